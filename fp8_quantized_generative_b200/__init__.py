@@ -16,8 +16,18 @@ Variants from the pages: activations in E5M2 (quantize_rows_dynamic(X,
 fmt="e5m2") with linear(..., x_fmt="e5m2")), per-tensor weight scales
 (quantize_weight_per_tensor) and 128x128 block-scaled MoE expert weights
 (quantize_weight_blockwise with moe_grouped_linear_blockscaled).
+
+Around the linears, the rest of an FFN block: bias, activation and residual in
+the linear's epilogue, the MoE router, and a whole MoE FFN for a few tokens.
+
+    Y = linear_epilogue(Xq, s_x, Wq, s_w, bias=b, activation="gelu", residual=R)
+    r = moe_route(logits, topk)                 # experts, weights, grouped row layout
+    out = moe_layer(X, r.experts, r.weights, Wq_up, s_up, Wq_down, s_down, activation="silu", gated=True)
 """
 from __future__ import annotations
+
+import contextlib
+from typing import NamedTuple
 
 import torch
 
@@ -30,6 +40,7 @@ __all__ = [
     "moe_grouped_linear_combine", "quantize_rows_dispatch", "quantized_linear_overlapped", "overlap_workspace",
     "moe_grouped_linear_blockscaled",
     "quantized_linear", "e4m3_encode_f32", "device_error", "set_gemm_tuning",
+    "linear_epilogue", "MoeRoute", "moe_route", "moe_layer", "moe_layer_workspace",
 ]
 
 
@@ -313,6 +324,162 @@ def moe_grouped_linear_blockscaled(Xq: torch.Tensor, s_x: torch.Tensor, offsets:
     check(_lib.fp8q_moe_grouped_linear_blockscaled(Xq.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), E, rows,
                                                    Wq.data_ptr(), s_wb.data_ptr(), N, K, Y.data_ptr(), _stream(Xq)),
           "fp8q_moe_grouped_linear_blockscaled")
+    return Y
+
+
+def _act(name) -> int:
+    try:
+        return _lib.ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {name!r} (none, relu, gelu, gelu_tanh or silu)") from None
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device made current for a call (the library launches on the current device)."""
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def linear_epilogue(Xq: torch.Tensor, s_x: torch.Tensor, Wq: torch.Tensor, s_w: torch.Tensor,
+                    bias: torch.Tensor | None = None, activation: str | None = None,
+                    residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    x_fmt: str = "e4m3") -> torch.Tensor:
+    """linear() with bias, activation and residual in its epilogue:
+    fp16(act(linear + bias) + residual), computed in fp32 and rounded once.
+    bias fp16 [N]; activation "none", "relu", "gelu", "gelu_tanh" or "silu";
+    residual fp16 [M,N], which may be `out` itself."""
+    act = _act(activation)
+    fmt = _fmt(x_fmt)
+    _need(Xq, torch.uint8, "Xq", 2)
+    _need(Wq, torch.uint8, "Wq", 2)
+    _need(s_x, torch.float32, "s_x", 1)
+    _need(s_w, torch.float32, "s_w", 1)
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    if Wq.shape[1] != K or s_x.shape[0] != M or s_w.shape[0] != N:
+        raise ValueError("shape mismatch")
+    if bias is not None:
+        _need(bias, torch.float16, "bias", 1)
+        if bias.shape[0] != N:
+            raise ValueError("bias must be [N]")
+    if residual is not None:
+        _need(residual, torch.float16, "residual", 2)
+        if residual.shape != (M, N):
+            raise ValueError("residual must be [M,N]")
+    if out is not None:
+        _need(out, torch.float16, "out", 2)
+        if out.shape != (M, N):
+            raise ValueError("out must be [M,N]")
+    _same_device(Xq, s_x=s_x, Wq=Wq, s_w=s_w, bias=bias, residual=residual, out=out)
+    with _on(Xq):
+        Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=Xq.device)
+        check(_lib.fp8q_linear_epilogue(Xq.data_ptr(), fmt, s_x.data_ptr(), Wq.data_ptr(), s_w.data_ptr(), M, N, K,
+                                        bias.data_ptr() if bias is not None else 0, act,
+                                        residual.data_ptr() if residual is not None else 0, Y.data_ptr(), _stream(Xq)),
+              "fp8q_linear_epilogue")
+    return Y
+
+
+class MoeRoute(NamedTuple):
+    """What moe_route returns; all on the device, T tokens, E experts, rows = T * topk."""
+    experts: torch.Tensor      # int32 [T, topk], best first
+    weights: torch.Tensor      # fp32 [T, topk]
+    offsets: torch.Tensor      # int32 [E+1]: grouped rows of expert e are offsets[e] .. offsets[e+1]-1
+    row_token: torch.Tensor    # int32 [rows]
+    row_weight: torch.Tensor   # fp32 [rows]
+    token_rows: torch.Tensor   # int32 [T, topk]: the grouped row of each (token, choice)
+
+
+def moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True) -> MoeRoute:
+    """MoE router on the device: the topk experts of each token from fp16 gate
+    logits [T,E] (ties to the lower expert), their softmax weights (over the
+    chosen logits, or over all with renormalize=False), and the expert-grouped
+    rows in the form that quantize_rows_dispatch (token_rows), the grouped
+    linears (offsets), the combine (row_token, row_weight) and moe_layer
+    (experts, weights) read."""
+    _need(logits, torch.float16, "logits", 2)
+    T, E = logits.shape
+    if not 1 <= topk <= min(8, E):
+        raise ValueError("topk must be in [1, min(8, E)]")
+    dev = logits.device
+    # one allocation for all outputs (each 16-byte aligned) and the workspace
+    rows = T * topk
+    pad = -(-rows // 4) * 4
+    offs = -(-(E + 1) // 4) * 4
+    with _on(logits):
+        words = int(_lib.fp8q_moe_route_workspace_words(T, E))
+        buf = torch.empty((5 * pad + offs + words,), dtype=torch.int32, device=dev)
+        experts, row_token, token_rows = buf[:rows], buf[pad:pad + rows], buf[2 * pad:2 * pad + rows]
+        weights = buf[3 * pad:3 * pad + rows].view(torch.float32)
+        row_weight = buf[4 * pad:4 * pad + rows].view(torch.float32)
+        offsets = buf[5 * pad:5 * pad + E + 1]
+        base = buf.data_ptr()
+        check(_lib.fp8q_moe_route(logits.data_ptr(), T, E, topk, int(bool(renormalize)), base, base + 12 * pad,
+                                  base + 20 * pad, base + 4 * pad, base + 16 * pad, base + 8 * pad,
+                                  base + 4 * (5 * pad + offs) if words else 0, _stream(logits)), "fp8q_moe_route")
+    return MoeRoute(experts.view(T, topk), weights.view(T, topk), offsets, row_token, row_weight,
+                    token_rows.view(T, topk))
+
+
+def moe_layer_workspace(T: int, topk: int, F: int, N: int, device) -> torch.Tensor:
+    """Workspace of moe_layer for up to T tokens (uint8); reusable across calls
+    that do not overlap on the GPU."""
+    return torch.empty((int(_lib.fp8q_moe_layer_workspace_bytes(T, topk, F, N)),), dtype=torch.uint8, device=device)
+
+
+def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_up: torch.Tensor, s_up: torch.Tensor,
+              Wq_down: torch.Tensor, s_down: torch.Tensor, activation: str | None = "silu", gated: bool = False,
+              residual: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """A whole MoE FFN for a few tokens (up to 128): X fp16 [T,K] and the
+    router's experts int32 / weights fp32 [T,topk] (-1: no expert) in, fp16
+    [T,N] out.  Wq_up uint8 [E,F,K], or [E,2F,K] with gated=True (rows 0..F-1
+    are activated and multiply rows F..2F-1), Wq_down uint8 [E,N,F], with
+    per-channel scales s_up, s_down from quantize_weight_per_channel; residual
+    fp16 [T,N] is added (it may be `out` itself).  Larger batches: moe_route and
+    the grouped linears."""
+    act = _act(activation)
+    _need(X, torch.float16, "X", 2)
+    _need(experts, torch.int32, "experts", 2)
+    _need(weights, torch.float32, "weights", 2)
+    _need(Wq_up, torch.uint8, "Wq_up", 3)
+    _need(s_up, torch.float32, "s_up", 2)
+    _need(Wq_down, torch.uint8, "Wq_down", 3)
+    _need(s_down, torch.float32, "s_down", 2)
+    T, K = X.shape
+    topk = experts.shape[1]
+    E, N, F = Wq_down.shape
+    up_rows = 2 * F if gated else F
+    if (experts.shape[0] != T or weights.shape != experts.shape or Wq_up.shape != (E, up_rows, K)
+            or s_up.shape != (E, up_rows) or s_down.shape != (E, N)):
+        raise ValueError("shape mismatch")
+    if residual is not None:
+        _need(residual, torch.float16, "residual", 2)
+        if residual.shape != (T, N):
+            raise ValueError("residual must be [T,N]")
+    if out is not None:
+        _need(out, torch.float16, "out", 2)
+        if out.shape != (T, N):
+            raise ValueError("out must be [T,N]")
+    _same_device(X, experts=experts, weights=weights, Wq_up=Wq_up, s_up=s_up, Wq_down=Wq_down, s_down=s_down,
+                 residual=residual, workspace=workspace, out=out)
+    need = int(_lib.fp8q_moe_layer_workspace_bytes(T, topk, F, N))
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace", 1)
+        if workspace.numel() < need:
+            raise ValueError("workspace does not fit this call")
+    with _on(X):
+        Y = out if out is not None else torch.empty((T, N), dtype=torch.float16, device=X.device)
+        ws = workspace if workspace is not None else torch.empty((need,), dtype=torch.uint8, device=X.device)
+        check(_lib.fp8q_moe_layer(X.data_ptr(), T, experts.data_ptr(), weights.data_ptr(), topk, E, Wq_up.data_ptr(),
+                                  s_up.data_ptr(), Wq_down.data_ptr(), s_down.data_ptr(), K, F, N, act,
+                                  int(bool(gated)), residual.data_ptr() if residual is not None else 0, Y.data_ptr(),
+                                  ws.data_ptr(), _stream(X)), "fp8q_moe_layer")
     return Y
 
 

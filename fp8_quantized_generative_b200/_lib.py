@@ -23,6 +23,9 @@ FP8Q_FMT_E4M3 = 0
 FP8Q_FMT_E5M2 = 1
 FORMATS = {"e4m3": FP8Q_FMT_E4M3, "e5m2": FP8Q_FMT_E5M2}
 
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # FP8Q_ACT_*
+MOE_LAYER_MAX_TOKENS = 128
+
 DEVERR_TIMEOUT_PRODUCER = 0x1
 DEVERR_TIMEOUT_MMA = 0x2
 DEVERR_TIMEOUT_EPILOGUE = 0x4
@@ -64,6 +67,12 @@ SIGNATURES = {
     "fp8q_moe_grouped_linear_combine": (_INT, [_P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P]),
     "fp8q_moe_grouped_linear_gather": (_INT, [_P, _P, _I64, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P]),
     "fp8q_moe_grouped_linear_blockscaled": (_INT, [_P, _P, _P, _I32, _I64, _P, _P, _I64, _I64, _P, _P]),
+    "fp8q_linear_epilogue": (_INT, [_P, _INT, _P, _P, _P, _I64, _I64, _I64, _P, _INT, _P, _P, _P]),
+    "fp8q_moe_route": (_INT, [_P, _I64, _I32, _I32, _INT, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "fp8q_moe_route_workspace_words": (_I64, [_I64, _I32]),
+    "fp8q_moe_layer": (_INT, [_P, _I64, _P, _P, _I32, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _INT, _P, _P, _P,
+                              _P]),
+    "fp8q_moe_layer_workspace_bytes": (_I64, [_I64, _I32, _I64, _I64]),
     "fp8q_e4m3_encode_f32": (_INT, [_P, _I64, _P, _P]),
     "fp8q_set_gemm_tuning": (_INT, [_INT, _INT, _INT]),
     "fp8q_selftest_wait_timeout": (_INT, [ctypes.c_uint32, _P]),
@@ -176,6 +185,30 @@ def fp8q_quantize_weight_blockwise(W, E, N, K, Wq, s_wb, stream):
 
 def fp8q_moe_grouped_linear_blockscaled(Xq, s_x, offsets, E, rows, Wq, s_wb, N, K, Y, stream):
     return lib().fp8q_moe_grouped_linear_blockscaled(Xq, s_x, offsets, E, rows, Wq, s_wb, N, K, Y, stream)
+
+
+def fp8q_linear_epilogue(Xq, x_fmt, s_x, Wq, s_w, M, N, K, bias, activation, residual, Y, stream):
+    return lib().fp8q_linear_epilogue(Xq, x_fmt, s_x, Wq, s_w, M, N, K, bias, activation, residual, Y, stream)
+
+
+def fp8q_moe_route(logits, T, E, topk, renormalize, experts, weights, offsets, row_token, row_weight, token_rows,
+                   workspace, stream):
+    return lib().fp8q_moe_route(logits, T, E, topk, renormalize, experts, weights, offsets, row_token, row_weight,
+                                token_rows, workspace, stream)
+
+
+def fp8q_moe_route_workspace_words(T, E):
+    return lib().fp8q_moe_route_workspace_words(T, E)
+
+
+def fp8q_moe_layer(X, T, experts, weights, topk, E, Wq_up, s_up, Wq_down, s_down, K, F, N, activation, gated, residual,
+                   out, workspace, stream):
+    return lib().fp8q_moe_layer(X, T, experts, weights, topk, E, Wq_up, s_up, Wq_down, s_down, K, F, N, activation,
+                                gated, residual, out, workspace, stream)
+
+
+def fp8q_moe_layer_workspace_bytes(T, topk, F, N):
+    return lib().fp8q_moe_layer_workspace_bytes(T, topk, F, N)
 
 
 def fp8q_e4m3_encode_f32(x, n, out, stream):

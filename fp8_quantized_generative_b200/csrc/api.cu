@@ -17,6 +17,8 @@
 #include "gemm_fp8_pair.cuh"
 #include "gemm_fp8_splitk.cuh"
 #include "gemm_fp8_blockscaled.cuh"
+#include "moe_few.cuh"
+#include "moe_route.cuh"
 #include "quant_rows.cuh"
 
 namespace fp8q {
@@ -230,7 +232,7 @@ cudaError_t launch_ex(void (*kernel)(Args...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool kGrouped, bool kGather = false>
+template <bool kGrouped, bool kGather = false, bool kEpi = false>
 fp8q_status launch_gemm(const uint8_t* A, int64_t a_rows, const uint8_t* B, int64_t b_rows, const GemmParams& p,
                         int64_t tiles_upper_bound, cudaStream_t st) {
   constexpr int BN = kGrouped ? kBNGrouped : kBN;
@@ -247,9 +249,9 @@ fp8q_status launch_gemm(const uint8_t* A, int64_t a_rows, const uint8_t* B, int6
   CUtensorMap ty;   // combine: Y is the [tokens, N] output, written by atomic adds only
   s = make_output_map(&ty, p.Y, p.comb_token != nullptr ? p.tokens : p.rows, p.N);
   if (s != FP8Q_OK) return s;
-  auto kernel = fp8_gemm_kernel<BN, STAGES, kGrouped, kGather>;
+  auto kernel = fp8_gemm_kernel<BN, STAGES, kGrouped, kGather, kEpi>;
   const size_t smem = L::smem_bytes(kGrouped ? p.E : 0);
-  e = ensure_smem<fp8_gemm_kernel<BN, STAGES, kGrouped, kGather>>(L::smem_bytes(kGrouped ? kMaxExperts : 0), dev);
+  e = ensure_smem<fp8_gemm_kernel<BN, STAGES, kGrouped, kGather, kEpi>>(L::smem_bytes(kGrouped ? kMaxExperts : 0), dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   const int grid = static_cast<int>(tiles_upper_bound < sms ? (tiles_upper_bound < 1 ? 1 : tiles_upper_bound) : sms);
   e = launch_ex(kernel, dim3(grid), dim3(kGemmThreads), smem, st, 1, true, ta, tb, ty, p);
@@ -334,7 +336,7 @@ TailSplit tail_split(int64_t full_tiles, int clusters, int bn) {
 // Launch a pair kernel.  Dense: A = Xq [rows, K], B = Wq [N, K].  Grouped:
 // B = Wq [E*N, K] and the schedule comes from the device offsets;
 // `tiles_upper_bound` caps the grid when the tile count is unknown on the host.
-template <int BN, int STAGES, bool kGrouped, bool kQuantA = false, int SK = kBK>
+template <int BN, int STAGES, bool kGrouped, bool kQuantA = false, int SK = kBK, bool kEpi = false>
 fp8q_status launch_pair(const uint8_t* A, const uint8_t* B, int64_t b_rows, const GemmParams& p0, int dev,
                         cudaStream_t st, int64_t tiles_upper_bound = 0) {
   using L = PairLayout<BN, STAGES, SK>;
@@ -373,8 +375,8 @@ fp8q_status launch_pair(const uint8_t* A, const uint8_t* B, int64_t b_rows, cons
   if (s != FP8Q_OK) return s;
   s = make_output_map(&ty, p.Y, p.rows, p.N);
   if (s != FP8Q_OK) return s;
-  auto kernel = fp8_gemm_pair_kernel<BN, STAGES, kGrouped, kQuantA, SK>;
-  cudaError_t e = ensure_smem<fp8_gemm_pair_kernel<BN, STAGES, kGrouped, kQuantA, SK>>(
+  auto kernel = fp8_gemm_pair_kernel<BN, STAGES, kGrouped, kQuantA, SK, kEpi>;
+  cudaError_t e = ensure_smem<fp8_gemm_pair_kernel<BN, STAGES, kGrouped, kQuantA, SK, kEpi>>(
       L::smem_bytes(kGrouped ? kMaxExperts : 0), dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(pair)");
   const int pairs = static_cast<int>(tiles < clusters ? (tiles < 1 ? 1 : tiles) : clusters);
@@ -477,7 +479,7 @@ int choose_ksplit(int dev, int n_tiles, int num_kb) {
 // Dense linear with at most 128 token rows.  kFused: A is the fp16
 // activations (p.x_f16) and the kernel quantizes them itself (<= 64 rows);
 // otherwise A is Xq with scales s_x.
-template <int MPAD, int STAGES, bool kFused, int SK = kBK>
+template <int MPAD, int STAGES, bool kFused, int SK = kBK, bool kEpi = false>
 fp8q_status launch_splitk(const uint8_t* Xq, const uint8_t* Wq, const GemmParams& p, int dev, cudaStream_t st) {
   using L = SplitKLayout<MPAD, STAGES, kFused, SK>;
   CUtensorMap tw, tx;
@@ -498,8 +500,8 @@ fp8q_status launch_splitk(const uint8_t* Xq, const uint8_t* Wq, const GemmParams
     return FP8Q_ERR_UNSUPPORTED;
   }
   const size_t smem = kFused ? L::fused_smem_bytes(nkb_max) : L::kSmemBytes;
-  auto kernel = fp8_gemm_splitk_kernel<MPAD, STAGES, kFused, SK>;
-  cudaError_t e = ensure_smem<fp8_gemm_splitk_kernel<MPAD, STAGES, kFused, SK>>(
+  auto kernel = fp8_gemm_splitk_kernel<MPAD, STAGES, kFused, SK, kEpi>;
+  cudaError_t e = ensure_smem<fp8_gemm_splitk_kernel<MPAD, STAGES, kFused, SK, kEpi>>(
       kFused ? L::fused_smem_bytes(L::kFusedMaxKBlocks) : L::kSmemBytes, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(splitk)");
   e = launch_ex(kernel, dim3(n_tiles * S), dim3(kSkThreads), smem, st, S, true, tw, tx, p);
@@ -507,6 +509,10 @@ fp8q_status launch_splitk(const uint8_t* Xq, const uint8_t* Wq, const GemmParams
   return FP8Q_OK;
 }
 
+// kEpi: the kernels with bias, activation and residual in the epilogue, in
+// their default stage forms only (the stage environment knobs and tile_n = 512
+// select forms of the plain linear).
+template <bool kEpi = false>
 fp8q_status launch_dense(const uint8_t* Xq, const uint8_t* Wq, const GemmParams& p, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = current_device_info(&dev, &sms);
@@ -524,22 +530,26 @@ fp8q_status launch_dense(const uint8_t* Xq, const uint8_t* Wq, const GemmParams&
     // against two-stage rings, and four-box stages M=1 7.09 -> 6.78 us,
     // M=8 7.40 -> 7.06, M=16 7.43 -> 7.11, M=32 7.94 -> 7.70 against those.
     // At 128 rows the partial exchange buffer leaves room for two stages.
-    const int sk = kn.splitk_stage_k ? kn.splitk_stage_k : (p.rows <= 32 ? 512 : 256);
+    const int sk = !kEpi && kn.splitk_stage_k ? kn.splitk_stage_k : (p.rows <= 32 ? 512 : 256);
     if (sk == 512 && p.rows <= 32) {
-      if (p.rows <= 16) return launch_splitk<16, 2, false, 512>(Xq, Wq, p, dev, st);
-      return launch_splitk<32, 2, false, 512>(Xq, Wq, p, dev, st);
+      if (p.rows <= 16) return launch_splitk<16, 2, false, 512, kEpi>(Xq, Wq, p, dev, st);
+      return launch_splitk<32, 2, false, 512, kEpi>(Xq, Wq, p, dev, st);
     }
     if (sk >= 256) {
-      if (p.rows <= 16) return launch_splitk<16, 4, false, 256>(Xq, Wq, p, dev, st);
-      if (p.rows <= 32) return launch_splitk<32, 4, false, 256>(Xq, Wq, p, dev, st);
-      if (p.rows <= 64) return launch_splitk<64, 3, false, 256>(Xq, Wq, p, dev, st);
-      if (p.rows <= 128) return launch_splitk<128, 2, false, 256>(Xq, Wq, p, dev, st);
+      if constexpr (!kEpi) {
+        if (p.rows <= 16) return launch_splitk<16, 4, false, 256>(Xq, Wq, p, dev, st);
+        if (p.rows <= 32) return launch_splitk<32, 4, false, 256>(Xq, Wq, p, dev, st);
+      }
+      if (p.rows <= 64) return launch_splitk<64, 3, false, 256, kEpi>(Xq, Wq, p, dev, st);
+      if (p.rows <= 128) return launch_splitk<128, 2, false, 256, kEpi>(Xq, Wq, p, dev, st);
     }
     // one-box stages (FP8Q_SPLITK_STAGE_K=128)
-    if (p.rows <= 16) return launch_splitk<16, 5, false>(Xq, Wq, p, dev, st);
-    if (p.rows <= 32) return launch_splitk<32, 4, false>(Xq, Wq, p, dev, st);
-    if (p.rows <= 64) return launch_splitk<64, 3, false>(Xq, Wq, p, dev, st);
-    if (p.rows <= 128) return launch_splitk<128, 4, false>(Xq, Wq, p, dev, st);
+    if constexpr (!kEpi) {
+      if (p.rows <= 16) return launch_splitk<16, 5, false>(Xq, Wq, p, dev, st);
+      if (p.rows <= 32) return launch_splitk<32, 4, false>(Xq, Wq, p, dev, st);
+      if (p.rows <= 64) return launch_splitk<64, 3, false>(Xq, Wq, p, dev, st);
+      if (p.rows <= 128) return launch_splitk<128, 4, false>(Xq, Wq, p, dev, st);
+    }
   }
   bool pair = p.rows > kBM;
   // Walk n-blocks first when A is the larger operand: each A block is then
@@ -560,6 +570,13 @@ fp8q_status launch_dense(const uint8_t* Xq, const uint8_t* Wq, const GemmParams&
     int bn = kn.bn ? kn.bn : choose_pair_bn(p.rows, p.N, clusters > 0 ? clusters : sms / 2);
     // Two 128-byte K boxes per stage (measured 3-10% faster on B200 than one:
     // the MMA-issuing thread's per-stage work is spread over eight MMAs).
+    if constexpr (kEpi) {
+      switch (bn) {
+        case 128: return launch_pair<128, 4, false, false, 256, true>(Xq, Wq, p.N, q, dev, st);
+        case 192: return launch_pair<192, 3, false, false, 256, true>(Xq, Wq, p.N, q, dev, st);
+        default: return launch_pair<256, 3, false, false, 256, true>(Xq, Wq, p.N, q, dev, st);
+      }
+    } else {
     if (kn.stage_k == 256) {
       switch (bn) {
         case 128: return launch_pair<128, 4, false, false, 256>(Xq, Wq, p.N, q, dev, st);
@@ -574,9 +591,10 @@ fp8q_status launch_dense(const uint8_t* Xq, const uint8_t* Wq, const GemmParams&
       case 512: return launch_pair<512, 4, false>(Xq, Wq, p.N, q, dev, st);
       default: return launch_pair<256, 6, false>(Xq, Wq, p.N, q, dev, st);
     }
+    }
   }
   const int64_t tiles = int64_t((p.rows + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
-  return launch_gemm<false>(Xq, p.rows, Wq, p.N, q, tiles, st);
+  return launch_gemm<false, false, kEpi>(Xq, p.rows, Wq, p.N, q, tiles, st);
 }
 
 fp8q_status check_quant_args(const void* X, int64_t M, int64_t K, const void* Q, const void* S) {
@@ -606,9 +624,25 @@ fp8q_status quantize(const void* X, int64_t M, int64_t K, uint8_t* Q, float* S, 
   return FP8Q_OK;
 }
 
-// Dense linear, activations in format x_fmt (weights E4M3).
+// The epilogue of fp8q_linear_epilogue.
+struct Epilogue {
+  const __half* bias = nullptr;
+  int act = kActNone;
+  const __half* residual = nullptr;
+};
+
+bool valid_act(int act) { return act >= kActNone && act <= kActSilu; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+// Dense linear, activations in format x_fmt (weights E4M3); epi: bias,
+// activation and residual (nullptr: the plain linear).
 fp8q_status linear_impl(const uint8_t* Xq, int x_fmt, const float* s_x, const uint8_t* Wq, const float* s_w,
-                        int64_t M, int64_t N, int64_t K, void* Y_f16, void* stream) {
+                        int64_t M, int64_t N, int64_t K, void* Y_f16, void* stream, const Epilogue* epi = nullptr) {
   if (!valid_fmt(x_fmt)) return invalid("x_fmt must be FP8Q_FMT_E4M3 or FP8Q_FMT_E5M2");
   if (M < 0 || M > kMaxDim) return invalid("M out of range");
   if (N <= 0 || N > kMaxDim || N % 8 != 0) return invalid("N must be positive and a multiple of 8");
@@ -630,7 +664,55 @@ fp8q_status linear_impl(const uint8_t* Xq, int x_fmt, const float* s_x, const ui
   p.tail_q = 1;
   p.l2_prefetch = l2_prefetch_enabled();
   p.x_fmt = x_fmt;
+  if (epi != nullptr) {
+    p.bias = epi->bias;
+    p.residual = epi->residual;
+    p.act = epi->act;
+    return launch_dense<true>(Xq, Wq, p, static_cast<cudaStream_t>(stream));
+  }
   return launch_dense(Xq, Wq, p, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ router
+template <int KPL, int THREADS>
+cudaError_t launch_route(const RouteParams& p, int dev, cudaStream_t st) {
+  const size_t smem = route_smem(p.E, THREADS / 32), max_smem = route_smem(32 * KPL, THREADS / 32);
+  cudaError_t e = ensure_smem<route_choose_kernel<KPL, THREADS>>(max_smem, dev);
+  if (e != cudaSuccess) return e;
+  e = launch_ex(route_choose_kernel<KPL, THREADS>, dim3(p.chunks), dim3(THREADS), smem, st, 1, true, p);
+  if (e != cudaSuccess || p.chunks == 1) return e;
+  constexpr int kPlaceThreads = 512;
+  e = ensure_smem<route_place_kernel<kPlaceThreads>>(route_smem(kRouteMaxExperts, kPlaceThreads / 32), dev);
+  if (e != cudaSuccess) return e;
+  return launch_ex(route_place_kernel<kPlaceThreads>, dim3(p.chunks), dim3(kPlaceThreads),
+                   route_smem(p.E, kPlaceThreads / 32), st, 1, true, p);
+}
+
+// ------------------------------------------------------------------ MoE layer for a few tokens
+// hidden rows fp16 [rows, F], then y fp32 [rows, N]
+int64_t moe_layer_y_offset(int64_t rows, int64_t F) { return (rows * F * 2 + 255) & ~int64_t(255); }
+
+template <int NT, int kDepth, bool kUp, bool kGated>
+fp8q_status launch_moe_few(MoeFewParams p, int dev, int sms, cudaStream_t st) {
+  const MoeFewLayout l = mf_layout(NT, kDepth, p.K, 8, p.rows, p.E);
+  const int fit = (kMfMaxSmem - l.total) / l.pitch / 8 * 8;
+  if (fit < 8) return invalid("fp8q_moe_layer: a row does not fit in shared memory");   // (K, F <= 8192 always fit)
+  p.rmax = fit < NT * 8 ? fit : NT * 8;
+  const size_t smem = size_t(l.total) + size_t(p.rmax) * l.pitch;
+  cudaError_t e = ensure_smem<moe_few_kernel<NT, kDepth, kUp, kGated>>(kMfMaxSmem, dev);
+  if (e == cudaSuccess)
+    e = launch_ex(moe_few_kernel<NT, kDepth, kUp, kGated>, dim3(sms), dim3(kMfThreads), smem, st, 1, true, p);
+  if (e != cudaSuccess) return cuda_fail(e, "moe_few_kernel launch");
+  return FP8Q_OK;
+}
+
+// n-tiles by the batch: an expert sees at most T rows (one a token).
+template <bool kUp, bool kGated>
+fp8q_status launch_moe_few_nt(const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
+  if (T <= 8) return launch_moe_few<1, 6, kUp, kGated>(p, dev, sms, st);
+  if (T <= 16) return launch_moe_few<2, 6, kUp, kGated>(p, dev, sms, st);
+  if (T <= 32) return launch_moe_few<4, 6, kUp, kGated>(p, dev, sms, st);
+  return launch_moe_few<8, 4, kUp, kGated>(p, dev, sms, st);
 }
 
 }  // namespace
@@ -763,6 +845,23 @@ fp8q_status fp8q_linear(const uint8_t* Xq, const float* s_x, const uint8_t* Wq, 
 fp8q_status fp8q_linear_fmt(const uint8_t* Xq, fp8q_format x_fmt, const float* s_x, const uint8_t* Wq,
                             const float* s_w, int64_t M, int64_t N, int64_t K, void* Y_f16, void* stream) {
   return linear_impl(Xq, x_fmt, s_x, Wq, s_w, M, N, K, Y_f16, stream);
+}
+
+fp8q_status fp8q_linear_epilogue(const uint8_t* Xq, fp8q_format x_fmt, const float* s_x, const uint8_t* Wq,
+                                 const float* s_w, int64_t M, int64_t N, int64_t K, const void* bias_f16,
+                                 fp8q_activation activation, const void* residual_f16, void* Y_f16, void* stream) {
+  if (!valid_act(activation)) return invalid("activation must be one of FP8Q_ACT_*");
+  if (M > 0 && M <= kMaxDim && N > 0 && N <= kMaxDim) {
+    if (bias_f16 != nullptr && !aligned16(bias_f16)) return invalid("bias pointer must be 16-byte aligned");
+    if (residual_f16 != nullptr && !aligned16(residual_f16)) return invalid("residual pointer must be 16-byte aligned");
+    if (residual_f16 != nullptr && residual_f16 != Y_f16 && overlap(residual_f16, 2 * M * N, Y_f16, 2 * M * N))
+      return invalid("residual must be the output itself or not overlap it");
+  }
+  Epilogue e;
+  e.bias = static_cast<const __half*>(bias_f16);
+  e.act = activation;
+  e.residual = static_cast<const __half*>(residual_f16);
+  return linear_impl(Xq, x_fmt, s_x, Wq, s_w, M, N, K, Y_f16, stream, &e);
 }
 
 fp8q_status fp8q_quantized_linear(const void* X_f16, const uint8_t* Wq, const float* s_w, int64_t M, int64_t N,
@@ -1002,6 +1101,122 @@ fp8q_status fp8q_moe_grouped_linear_combine(const uint8_t* Xq, const float* s_x,
   p.comb_weight = row_weight;
   const int64_t tiles = ((rows + kBM - 1) / kBM + E) * ((N + kBNGrouped - 1) / kBNGrouped);
   return launch_gemm<true>(Xq, rows, Wq, int64_t(E) * N, p, tiles, st);
+}
+
+int64_t fp8q_moe_route_workspace_words(int64_t T, int32_t E) {
+  if (T <= kRouteOneCtaTokens || E < 1) return 0;
+  const int64_t chunk = route_chunk(T);
+  return (T + chunk - 1) / chunk * E;
+}
+
+fp8q_status fp8q_moe_route(const void* logits_f16, int64_t T, int32_t E, int32_t topk, int renormalize,
+                           int32_t* experts, float* weights, int32_t* offsets, int32_t* row_token, float* row_weight,
+                           int32_t* token_rows, int32_t* workspace, void* stream) {
+  if (E < 1 || E > kRouteMaxExperts) return invalid("E must be in [1, 1024]");
+  if (topk < 1 || topk > kRouteMaxTopk || topk > E) return invalid("topk must be in [1, min(8, E)]");
+  if (T < 0 || T > (int64_t(1) << 22)) return invalid("T must be in [0, 2^22]");
+  if (!aligned16(offsets)) return invalid("null or non-16-byte-aligned offsets");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const cudaError_t e = cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (size_t(E) + 1), st);
+    if (e != cudaSuccess) return cuda_fail(e, "offsets clear");
+    return FP8Q_OK;
+  }
+  if (!aligned16(logits_f16) || !aligned16(experts) || !aligned16(weights) || !aligned16(row_token) ||
+      !aligned16(row_weight) || !aligned16(token_rows))
+    return invalid("null or non-16-byte-aligned pointer");
+  if (T > kRouteOneCtaTokens && !aligned16(workspace)) return invalid("null or non-16-byte-aligned workspace");
+  int dev = 0, sms = 0;
+  cudaError_t e = current_device_info(&dev, &sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  RouteParams p = {};
+  p.logits = static_cast<const __half*>(logits_f16);
+  p.T = static_cast<int>(T);
+  p.E = E;
+  p.topk = topk;
+  p.renormalize = renormalize != 0;
+  p.chunk = route_chunk(T);
+  p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
+  p.experts = experts;
+  p.weights = weights;
+  p.offsets = offsets;
+  p.row_token = row_token;
+  p.row_weight = row_weight;
+  p.token_rows = token_rows;
+  p.counts = workspace;
+  // keys per lane; past 256 experts 512 threads, so that they stay in registers
+  if (E <= 64) e = launch_route<2, 1024>(p, dev, st);
+  else if (E <= 128) e = launch_route<4, 1024>(p, dev, st);
+  else if (E <= 256) e = launch_route<8, 1024>(p, dev, st);
+  else if (E <= 512) e = launch_route<16, 512>(p, dev, st);
+  else e = launch_route<32, 512>(p, dev, st);
+  if (e != cudaSuccess) return cuda_fail(e, "moe_route launch");
+  return FP8Q_OK;
+}
+
+int64_t fp8q_moe_layer_workspace_bytes(int64_t T, int32_t topk, int64_t F, int64_t N) {
+  if (T < 0 || topk < 1 || F < 1 || N < 1) return 0;
+  return moe_layer_y_offset(T * topk, F) + T * topk * N * 4;
+}
+
+fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts, const float* weights, int32_t topk,
+                           int32_t E, const uint8_t* Wq_up, const float* s_up, const uint8_t* Wq_down,
+                           const float* s_down, int64_t K, int64_t F, int64_t N, fp8q_activation activation,
+                           int gated, const void* residual_f16, void* out_f16, void* workspace, void* stream) {
+  if (!valid_act(activation)) return invalid("activation must be one of FP8Q_ACT_*");
+  if (E < 1 || E > kMfMaxExperts) return invalid("E must be in [1, 1024]");
+  if (topk < 1 || topk > kMfMaxTopk) return invalid("topk must be in [1, 8]");
+  if (T < 0 || T > FP8Q_MOE_LAYER_MAX_TOKENS)
+    return invalid("T must be in [0, 128] (larger batches: the grouped linears)");
+  if (K <= 0 || K > 8192 || K % 16 != 0) return invalid("K must be a positive multiple of 16, at most 8192");
+  if (F <= 0 || F > 8192 || F % 16 != 0) return invalid("F must be a positive multiple of 16, at most 8192");
+  if (N <= 0 || N > (1 << 20) || N % 8 != 0) return invalid("N must be a positive multiple of 8, at most 2^20");
+  if (T == 0) return FP8Q_OK;
+  if (!aligned16(X_f16) || !aligned16(Wq_up) || !aligned16(s_up) || !aligned16(Wq_down) || !aligned16(s_down) ||
+      !aligned16(out_f16) || !aligned16(workspace))
+    return invalid("null or non-16-byte-aligned pointer");
+  if (experts == nullptr || (reinterpret_cast<uintptr_t>(experts) & 3u) != 0) return invalid("experts pointer");
+  if (weights == nullptr || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return invalid("weights pointer");
+  if (residual_f16 != nullptr) {
+    if (!aligned16(residual_f16)) return invalid("residual pointer must be 16-byte aligned");
+    if (residual_f16 != out_f16 && overlap(residual_f16, 2 * T * N, out_f16, 2 * T * N))
+      return invalid("residual must be the output itself or not overlap it");
+  }
+  int dev = 0, sms = 0;
+  cudaError_t ce = current_device_info(&dev, &sms);
+  if (ce != cudaSuccess) return cuda_fail(ce, "device query");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t rows = T * topk;
+  MoeFewParams p = {};
+  p.x = static_cast<const __half*>(X_f16);
+  p.experts = experts;
+  p.w = Wq_up;
+  p.s_w = s_up;
+  p.rows = static_cast<int>(rows);
+  p.topk = topk;
+  p.E = E;
+  p.K = static_cast<int>(K);
+  p.n_out = static_cast<int>(F);
+  p.act = activation;
+  p.hidden = static_cast<__half*>(workspace);
+  p.y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + moe_layer_y_offset(rows, F));
+  fp8q_status s = gated ? launch_moe_few_nt<true, true>(p, T, dev, sms, st)
+                        : launch_moe_few_nt<true, false>(p, T, dev, sms, st);
+  if (s != FP8Q_OK) return s;
+  p.x = p.hidden;
+  p.w = Wq_down;
+  p.s_w = s_down;
+  p.K = static_cast<int>(F);
+  p.n_out = static_cast<int>(N);
+  s = launch_moe_few_nt<false, false>(p, T, dev, sms, st);
+  if (s != FP8Q_OK) return s;
+  const int64_t items = T * (N >> 2);
+  const int grid = static_cast<int>(items < 256 * int64_t(sms) ? (items + 255) / 256 : sms);
+  ce = launch_ex(moe_few_combine_kernel, dim3(grid), dim3(256), 0, st, 1, true, static_cast<const float*>(p.y), experts,
+                 weights, static_cast<const __half*>(residual_f16), static_cast<int>(T), static_cast<int>(topk),
+                 static_cast<int>(E), static_cast<int>(N), static_cast<__half*>(out_f16));
+  if (ce != cudaSuccess) return cuda_fail(ce, "moe_few_combine_kernel launch");
+  return FP8Q_OK;
 }
 
 fp8q_status fp8q_quantize_weight_blockwise(const void* W_f16, int32_t E, int64_t N, int64_t K, uint8_t* Wq,

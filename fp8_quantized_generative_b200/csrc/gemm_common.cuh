@@ -10,6 +10,7 @@
 
 #include <cuda.h>
 
+#include "activation.cuh"
 #include "ptx.cuh"
 
 namespace fp8q {
@@ -56,6 +57,11 @@ struct GemmParams {
   uint8_t* q_out;
   float* s_out;
   uint32_t* sync;
+  // Dense linear with an epilogue (the kEpi kernels):
+  // y = fp16(act(acc * s_x * s_w + bias) + residual).
+  const __half* bias;       // [N] (nullptr: none)
+  const __half* residual;   // [rows, N] (nullptr: none); may be Y itself
+  int act;                  // Activation
 };
 
 // Row of the activation codes / scales that product row r reads (the row
@@ -125,11 +131,12 @@ template <int kMaxChunks>
 struct EpiScales {
   float sx;
   float sw[kMaxChunks];
+  float sb[kMaxChunks];   // kEpi: the bias of the same columns
   float rw;    // combine: weight of this lane's row
   int ctok;    // combine: output (token) row of this lane's row, -1: none
 };
 
-template <int kMaxChunks>
+template <int kMaxChunks, bool kEpi = false>
 __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& t, const GemmParams& p,
                                                                  const EpiWarpView& w, int lane) {
   EpiScales<kMaxChunks> e;
@@ -152,8 +159,57 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
   for (int j = 0; j < kMaxChunks; ++j) {
     const int cl = w.col0 + j * 32 + lane;
     e.sw[j] = (j < w.nch && t.n0 + cl < p.N) ? __ldg(p.s_w + t.sw0 + cl) : 0.0f;
+    // no bias: adding -0 leaves every value, -0 included, as it is
+    if (kEpi) e.sb[j] = (p.bias != nullptr && j < w.nch && t.n0 + cl < p.N) ? __half2float(__ldg(p.bias + t.n0 + cl)) : -0.0f;
   }
   return e;
+}
+
+// The epilogue of the dense linear with bias, activation and residual, on the
+// 32 columns of one chunk that a lane holds: z = (acc * s_x) * s_w as the
+// plain linear computes it, then z + bias, the activation, + residual, each
+// fp32 and rounded to nearest; the caller rounds once to fp16.  `res` holds
+// the lane's 32 residual values (used when p.residual is set).
+template <int kMaxChunks>
+__device__ __forceinline__ void epilogue_values(float (&z)[32], const GemmParams& p, const EpiScales<kMaxChunks>& pre,
+                                                int j, const uint4 (&res)[4]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float w = __shfl_sync(0xffffffffu, pre.sw[j], i);
+    const float b = __shfl_sync(0xffffffffu, pre.sb[j], i);
+    z[i] = __fadd_rn(__fmul_rn(__fmul_rn(z[i], pre.sx), w), b);
+  }
+  switch (p.act) {   // uniform: one branch per chunk
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActRelu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActGelu);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActGeluTanh);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActSilu);
+      break;
+    default: break;
+  }
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const __half2* h = reinterpret_cast<const __half2*>(&res[c]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(h[i]);
+        z[c * 8 + 2 * i] = __fadd_rn(z[c * 8 + 2 * i], f.x);
+        z[c * 8 + 2 * i + 1] = __fadd_rn(z[c * 8 + 2 * i + 1], f.y);
+      }
+    }
+  }
 }
 
 // One epilogue warp drains its view (above), 32 columns at a time:
@@ -169,7 +225,10 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
 // scales per chunk and waited out every load and store measured no faster
 // on the dense shapes and up to 12% slower on the MoE kernels.)
 // w.nch <= kMaxChunks.
-template <int kMaxChunks, int kBufs>
+// kEpi: bias, activation and residual (epilogue_values).  A lane reads the
+// residual of its own row, 64 bytes a chunk, before the chunk is stored by
+// the same warp, so the residual may be Y itself.
+template <int kMaxChunks, int kBufs, bool kEpi = false>
 __device__ __forceinline__ void epilogue_slab(const EpiTile& t, const GemmParams& p, const CUtensorMap* tmY,
                                               uint32_t tmem_acc, const EpiWarpView& w, int warp, int lane,
                                               uint8_t* stage, const EpiScales<kMaxChunks>& pre) {
@@ -199,6 +258,25 @@ __device__ __forceinline__ void epilogue_slab(const EpiTile& t, const GemmParams
     const uint32_t* cur = v[j & 1];
     if (j + 1 < nch) tmem_ld_32x32b_x32(taddr0 + static_cast<uint32_t>((j + 1) * 32), v[(j + 1) & 1]);
     uint32_t packed[16];
+    if constexpr (kEpi) {
+      uint4 res[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int gcol = t.n0 + cl + c * 8;
+        res[c] = make_uint4(0, 0, 0, 0);
+        if (p.residual != nullptr && lane < valid && gcol < p.N)
+          res[c] = ld_global_v4(p.residual + static_cast<int64_t>(qrow0 + lane) * p.N + gcol);
+      }
+      float z[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(cur[i]);
+      epilogue_values<kMaxChunks>(z, p, pre, j, res);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const __half2 hv = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
+        packed[i] = *reinterpret_cast<const uint32_t*>(&hv);
+      }
+    } else
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float w0 = __shfl_sync(0xffffffffu, pre.sw[j], 2 * i);

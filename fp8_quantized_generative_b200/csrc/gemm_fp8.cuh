@@ -99,7 +99,7 @@ __device__ __forceinline__ TileCoord decode_tile(int t, const GemmParams& p, int
   return c;
 }
 
-template <int BN, int STAGES, bool kGrouped, bool kGather = false>
+template <int BN, int STAGES, bool kGrouped, bool kGather = false, bool kEpi = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
@@ -361,14 +361,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       et.sw0 = c.sw0;
       et.clip = !kGrouped;   // dense: rows past the end are past the tensor
       const EpiWarpView wv = epi_view(et, warp, BN, false);
-      const EpiScales<BN / 64> sc = epilogue_scales<BN / 64>(et, p, wv, lane);
+      const EpiScales<BN / 64> sc = epilogue_scales<BN / 64, kEpi>(et, p, wv, lane);
       if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
         raise_error(0x4u);
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      epilogue_slab<BN / 64, L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
+      epilogue_slab<BN / 64, L::kEpiBufs, kEpi>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
                                           stage, sc);
       tc_fence_before();
       __syncwarp();

@@ -121,7 +121,8 @@ __device__ __forceinline__ PairTile pair_tile(int t, const GemmParams& p, int nu
   return r;
 }
 
-template <int BN, int STAGES, bool kGrouped, bool kQuantA = false, int SK = kBK>
+// kEpi (dense): bias, activation and residual in the epilogue.
+template <int BN, int STAGES, bool kGrouped, bool kQuantA = false, int SK = kBK, bool kEpi = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAh,
                          const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBt,
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       et.sw0 = pt.sw0;
       et.clip = !kGrouped;   // dense: rows past the end are past the tensor
       const EpiWarpView wv = epi_view(et, warp, pt.bn, pt.half);
-      EpiScales<BN / 64> sc = epilogue_scales<BN / 64>(et, p, wv, lane);
+      EpiScales<BN / 64> sc = epilogue_scales<BN / 64, kEpi>(et, p, wv, lane);
       if (kQuantA) {
         // the row scales were written in this kernel: read them once the
         // block is complete (it is before its first MMA, so this wait ends)
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         break;
       }
       tc_fence_after();
-      epilogue_slab<BN / 64, L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
+      epilogue_slab<BN / 64, L::kEpiBufs, kEpi>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
                                           stage, sc);
       tc_fence_before();
       __syncwarp();

@@ -83,8 +83,10 @@ struct SplitKLayout {
 // receive buffer) summed in rank order 0..S-1, scaled and stored as fp16.
 // Each of the 128 epilogue threads takes blocks of 4 token rows x 8 weight
 // rows: eight 16-byte shared loads per slice, one 16-byte global store per
-// token row (the 8 outputs are consecutive columns of Y).
-template <int S, typename L>
+// token row (the 8 outputs are consecutive columns of Y).  kEpi: bias,
+// activation and residual after the scales (the residual is read by the
+// thread that then writes the same 8 outputs, so it may be Y itself).
+template <int S, typename L, bool kEpi>
 __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const float* send, const float* recv,
                                                     const float* sc_w, const float* sc_x, int n0, int rank, int et) {
   constexpr int SL = kBM / S;
@@ -100,6 +102,14 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
     const int nl0 = (idx / m4n) * 8;
     const int n = n0 + rank * SL + nl0;
     if (n >= p.N) continue;                        // N % 8 == 0: a block is all in or all out
+    uint4 res[4], bias = make_uint4(0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u);   // -0: adds nothing
+    if constexpr (kEpi) {
+      if (p.bias != nullptr) bias = __ldg(reinterpret_cast<const uint4*>(p.bias + n));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p.residual != nullptr && m + i < p.rows)
+          res[i] = ld_global_v4(p.residual + static_cast<int64_t>(m + i) * p.N + n);
+    }
     float acc[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
@@ -124,6 +134,21 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
       if (m + i >= p.rows) break;
       const float sx = sc_x[m + i];
       uint32_t w[4];
+      if constexpr (kEpi) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 b = __half22float2(reinterpret_cast<const __half2*>(&bias)[j / 2]);
+          float y0 = activate(__fadd_rn(__fmul_rn(__fmul_rn(acc[j][i], sx), sw[j]), b.x), p.act);
+          float y1 = activate(__fadd_rn(__fmul_rn(__fmul_rn(acc[j + 1][i], sx), sw[j + 1]), b.y), p.act);
+          if (p.residual != nullptr) {
+            const float2 r = __half22float2(reinterpret_cast<const __half2*>(&res[i])[j / 2]);
+            y0 = __fadd_rn(y0, r.x);
+            y1 = __fadd_rn(y1, r.y);
+          }
+          const __half2 h = __floats2half2_rn(y0, y1);
+          w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      } else
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const __half2 h = __floats2half2_rn(__fmul_rn(__fmul_rn(acc[j][i], sx), sw[j]),
@@ -135,7 +160,7 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
   }
 }
 
-template <int MPAD, int STAGES, bool kFused, int SK = kBK>
+template <int MPAD, int STAGES, bool kFused, int SK = kBK, bool kEpi = false>
 __global__ void __launch_bounds__(kSkThreads, 1)
     fp8_gemm_splitk_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                            const GemmParams p) {
@@ -492,10 +517,10 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       *abort_flag = 1;
     } else {
       switch (S) {
-        case 1: splitk_reduce_store<1, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
-        case 2: splitk_reduce_store<2, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
-        case 4: splitk_reduce_store<4, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
-        default: splitk_reduce_store<8, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        case 1: splitk_reduce_store<1, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        case 2: splitk_reduce_store<2, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        case 4: splitk_reduce_store<4, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        default: splitk_reduce_store<8, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
       }
     }
   }

@@ -1,0 +1,280 @@
+// Router of the mixture of experts: from the gate's fp16 logits [T, E] to the
+// top-k experts of every token, their combine weights, and the expert-grouped
+// row layout that the dispatch quantizer, the grouped linears and the combine
+// read -- all on the device, so a step needs no host round trip.
+//
+// Selection: the k largest logits, ties to the lower expert.  A logit becomes a
+// 32-bit key whose unsigned order is that rule: the order-preserving 16-bit
+// image of the fp16 value (-0 as +0, NaN below -inf) over the complemented
+// expert index, so one redux.sync maximum per choice finds value and expert.
+// Weights (fp32): exp(l_j - l_max) over the sum of the same over the chosen
+// experts, or over all of them; the maximum itself counts as 1, so a token whose
+// largest logit is +inf shares its weight among the experts that have it, and a
+// token without any logit above -inf gets weight 0 everywhere.
+// Grouping: rows ordered by (expert, token): a counting sort.  Every warp takes
+// a run of consecutive tokens and counts its rows per expert in a table of its
+// own; prefix sums over warps, chunks of tokens and experts turn the counts into
+// first rows, and the second walk over the same tokens hands the rows out in
+// order.  No atomic's order reaches a result.
+//
+// Bound: launch and latency at few tokens (one CTA does it all, in one
+// launch); above that two launches, the counts of all chunks in between.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace fp8q {
+
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopk = 8;
+constexpr int kRouteOneCtaTokens = 64;    // at most: one CTA, one launch
+constexpr int kRouteMaxChunks = 128;      // CTAs of the two-launch form
+
+struct RouteParams {
+  const __half* logits;   // [T, E]
+  int T, E, topk;
+  int renormalize;        // 1: weights sum to 1 over the chosen experts; 0: softmax over all experts
+  int chunk;              // tokens per CTA
+  int chunks;             // CTAs
+  int32_t* experts;       // [T, topk]
+  float* weights;         // [T, topk]
+  int32_t* offsets;       // [E + 1]
+  int32_t* row_token;     // [T * topk]
+  float* row_weight;      // [T * topk]
+  int32_t* token_rows;    // [T, topk]
+  int32_t* counts;        // [chunks, E] workspace of the two-launch form
+};
+
+inline int route_chunk(int64_t T) {
+  const int64_t c = (T + kRouteMaxChunks - 1) / kRouteMaxChunks;
+  return static_cast<int>(T <= kRouteOneCtaTokens ? (T < 1 ? 1 : T) : c < 32 ? 32 : c);
+}
+
+// fp16 bits -> 16-bit unsigned of the same order; NaN -> 0, -0 -> +0.
+__device__ __forceinline__ uint32_t route_order(uint32_t h) {
+  if ((h & 0x7fffu) > 0x7c00u) return 0u;
+  if (h == 0x8000u) h = 0u;
+  return (h & 0x8000u) ? (~h & 0xffffu) : (h | 0x8000u);
+}
+// The logit of a key (NaN: -inf, which weighs nothing).
+__device__ __forceinline__ float route_logit(uint32_t key) {
+  const uint32_t o = key >> 16;
+  const uint32_t h = o == 0u ? 0xfc00u : (o & 0x8000u) ? (o & 0x7fffu) : (~o & 0xffffu);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+}
+// exp(l - m) of the softmax; m is the token's largest logit.
+__device__ __forceinline__ float route_exp(float l, float m) {
+  if (m == -INFINITY) return 0.0f;
+  return l == m ? 1.0f : expf(l - m);
+}
+
+// Tokens [first, last) of this warp within its CTA's chunk.
+struct RouteSpan {
+  int first, last;
+};
+__device__ __forceinline__ RouteSpan route_span(const RouteParams& p, int warp, int warps) {
+  const int c0 = static_cast<int>(blockIdx.x) * p.chunk;
+  const int n = min(p.chunk, p.T - c0);
+  const int per = (n + warps - 1) / warps;
+  RouteSpan s;
+  s.first = c0 + min(n, warp * per);
+  s.last = c0 + min(n, (warp + 1) * per);
+  return s;
+}
+
+// Choose the experts of this warp's tokens; count them per expert in `hist`.
+template <int KPL>
+__device__ __forceinline__ void route_choose(const RouteParams& p, const RouteSpan& s, uint16_t* hist, int lane) {
+  for (int t = s.first; t < s.last; ++t) {
+    const unsigned short* src = reinterpret_cast<const unsigned short*>(p.logits + static_cast<int64_t>(t) * p.E);
+    uint32_t key[KPL];
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = e < p.E ? (route_order(__ldg(src + e)) << 16) | (0xffffu - static_cast<uint32_t>(e)) : 0u;
+    }
+    float all = 0.0f, m = 0.0f;
+    uint32_t mine = 0;   // lane j: the j-th choice
+    for (int j = 0; j < p.topk; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) best = max(best, key[i]);
+      best = __reduce_max_sync(0xffffffffu, best);
+      if (j == 0) {
+        m = route_logit(best);
+        if (!p.renormalize) {
+#pragma unroll
+          for (int i = 0; i < KPL; ++i)
+            if (key[i] != 0u) all += route_exp(route_logit(key[i]), m);
+        }
+      }
+      if (lane == j) mine = best;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i)
+        if (key[i] == best) key[i] = 0u;
+    }
+    const bool have = lane < p.topk;
+    const float z = have ? route_exp(route_logit(mine), m) : 0.0f;
+    float sum = p.renormalize ? z : all;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (have) {
+      const int e = static_cast<int>(0xffffu - (mine & 0xffffu));
+      const int64_t at = static_cast<int64_t>(t) * p.topk + lane;
+      p.experts[at] = e;
+      p.weights[at] = sum > 0.0f ? __fdiv_rn(z, sum) : 0.0f;
+      ++hist[e];   // a token's experts are distinct: no two lanes share a counter
+    }
+    __syncwarp();
+  }
+}
+
+// hist[w][e] -> rows of expert e in the warps before w; total[e] -> their sum.
+__device__ __forceinline__ void route_warp_prefix(const RouteParams& p, uint16_t* hist, int* total, int warps) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int acc = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int c = hist[w * p.E + e];
+      hist[w * p.E + e] = static_cast<uint16_t>(acc);
+      acc += c;
+    }
+    total[e] = acc;
+  }
+}
+
+// Exclusive prefix sum over the experts by one warp: first[e] and, at [E], the sum.
+__device__ __forceinline__ void route_expert_prefix(int E, const int* total, int* first, int lane) {
+  const int per = (E + 31) / 32;
+  const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) sum += total[e];
+  int acc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, acc, o);
+    if (lane >= o) acc += v;
+  }
+  int at = acc - sum;
+  for (int e = e0; e < e1; ++e) {
+    const int c = total[e];   // (total may be first)
+    first[e] = at;
+    at += c;
+  }
+  if (lane == 31) first[E] = acc;
+}
+
+// Hand out the rows of this warp's tokens in order.  base[e]: the first row of
+// expert e in this chunk; hist[e]: this warp's next row within it.
+__device__ __forceinline__ void route_place(const RouteParams& p, const RouteSpan& s, uint16_t* hist, const int* base,
+                                            int lane) {
+  for (int t = s.first; t < s.last; ++t) {
+    if (lane < p.topk) {
+      const int64_t at = static_cast<int64_t>(t) * p.topk + lane;
+      const int e = p.experts[at];
+      const float w = p.weights[at];
+      const int row = base[e] + hist[e]++;
+      p.token_rows[at] = row;
+      p.row_token[row] = t;
+      p.row_weight[row] = w;
+    }
+    __syncwarp();
+  }
+}
+
+// Shared memory: per-warp counters [warps][E] uint16, then two int tables [E + 1].
+inline size_t route_smem(int E, int warps) {
+  return ((static_cast<size_t>(warps) * E * 2 + 15) & ~size_t(15)) + 2 * static_cast<size_t>(E + 1) * 4;
+}
+struct RouteTables {
+  uint16_t* hist;
+  int* total;
+  int* first;
+};
+__device__ __forceinline__ RouteTables route_tables(uint8_t* smem, int E, int warps) {
+  RouteTables r;
+  r.hist = reinterpret_cast<uint16_t*>(smem);
+  r.total = reinterpret_cast<int*>(smem + ((static_cast<size_t>(warps) * E * 2 + 15) & ~size_t(15)));
+  r.first = r.total + (E + 1);
+  return r;
+}
+
+// First launch: choices and counts.  With one chunk it goes on to place the rows.
+template <int KPL, int THREADS>
+__global__ void __launch_bounds__(THREADS) route_choose_kernel(const RouteParams p) {
+  extern __shared__ __align__(16) uint8_t route_smem_raw[];
+  constexpr int kWarps = THREADS / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RouteTables tb = route_tables(route_smem_raw, p.E, kWarps);
+  for (int i = threadIdx.x; i < kWarps * p.E; i += THREADS) tb.hist[i] = 0;
+  __syncthreads();
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const RouteSpan s = route_span(p, warp, kWarps);
+  uint16_t* hist = tb.hist + warp * p.E;
+  route_choose<KPL>(p, s, hist, lane);
+  __syncthreads();
+  route_warp_prefix(p, tb.hist, tb.total, kWarps);
+  __syncthreads();
+  if (p.chunks > 1) {
+    for (int e = threadIdx.x; e < p.E; e += THREADS)
+      p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = tb.total[e];
+    return;
+  }
+  if (warp == 0) route_expert_prefix(p.E, tb.total, tb.first, lane);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += THREADS) p.offsets[e] = tb.first[e];
+  route_place(p, s, hist, tb.first, lane);
+}
+
+// Second launch: the first row of every (chunk, expert) from the counts of all
+// chunks, then the rows of this chunk.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams p) {
+  extern __shared__ __align__(16) uint8_t route_smem_raw[];
+  constexpr int kWarps = THREADS / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RouteTables tb = route_tables(route_smem_raw, p.E, kWarps);
+  for (int i = threadIdx.x; i < kWarps * p.E; i += THREADS) tb.hist[i] = 0;
+  for (int e = threadIdx.x; e <= p.E; e += THREADS) tb.total[e] = tb.first[e] = 0;
+  __syncthreads();
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  // rows of each expert in the chunks before this one (first) and in all (total)
+  const int parts = max(1, THREADS / p.E);
+  for (int i = threadIdx.x; i < parts * p.E; i += THREADS) {
+    const int e = i % p.E;
+    int before = 0, sum = 0;
+    for (int c = i / p.E; c < p.chunks; c += parts) {
+      const int v = p.counts[static_cast<int64_t>(c) * p.E + e];
+      sum += v;
+      if (c < static_cast<int>(blockIdx.x)) before += v;
+    }
+    atomicAdd(&tb.total[e], sum);      // integers: the order does not matter
+    atomicAdd(&tb.first[e], before);
+  }
+  // this warp's rows per expert
+  const RouteSpan s = route_span(p, warp, kWarps);
+  uint16_t* hist = tb.hist + warp * p.E;
+  for (int t = s.first; t < s.last; ++t) {
+    if (lane < p.topk) ++hist[p.experts[static_cast<int64_t>(t) * p.topk + lane]];
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == 0) route_expert_prefix(p.E, tb.total, tb.total, lane);   // total[e] -> first row of expert e
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= p.E; e += THREADS) p.offsets[e] = tb.total[e];
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    tb.first[e] += tb.total[e];
+    int acc = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = tb.hist[w * p.E + e];
+      tb.hist[w * p.E + e] = static_cast<uint16_t>(acc);
+      acc += c;
+    }
+  }
+  __syncthreads();
+  route_place(p, s, hist, tb.first, lane);
+}
+
+}  // namespace fp8q

@@ -420,6 +420,17 @@ __device__ __forceinline__ float ld_relaxed_gpu_f32(const float* ptr) {
   return v;
 }
 
+// 16-byte coherent load (never the read-only data path): for memory that the
+// same kernel may also write.
+__device__ __forceinline__ uint4 ld_global_v4(const void* ptr) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(ptr)
+               : "memory");
+  return v;
+}
+
 // 2-D tiled bulk tensor store shared -> global (elements outside the tensor
 // are not written).  x is the innermost coordinate in elements.
 __device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t x, int32_t y) {

@@ -333,6 +333,97 @@ fp8q_status fp8q_moe_grouped_linear_fmt(const uint8_t* Xq, fp8q_format x_fmt, co
                                         int64_t N, int64_t K,
                                         void* Y_f16, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The FFN blocks around the linears (no counterpart on the pages, which name
+ * the linears alone): bias, activation and residual in the dense linear's
+ * epilogue, the MoE router, and a whole MoE FFN for a few tokens.  Same
+ * conventions as above; inputs are finite unless a function says otherwise.
+ */
+
+/* Activations, computed in fp32 (error far below half an fp16 step). */
+typedef enum {
+  FP8Q_ACT_NONE = 0,
+  FP8Q_ACT_RELU = 1,
+  FP8Q_ACT_GELU = 2,        /* z Phi(z), Phi the normal distribution function  */
+  FP8Q_ACT_GELU_TANH = 3,   /* 0.5 z (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) */
+  FP8Q_ACT_SILU = 4         /* z / (1 + exp(-z))                              */
+} fp8q_activation;
+
+/*
+ * fp8q_linear_fmt with an epilogue:
+ *   z = (acc * s_x[m]) * s_w[n] + bias[n]
+ *   Y[m,n] = fp16_rn( activation(z) + residual[m,n] )
+ * in fp32 with one rounding to fp16.  bias_f16 [N] and residual_f16 [M,N]
+ * fp16, either may be NULL (left out); without both and with FP8Q_ACT_NONE
+ * the result is fp8q_linear_fmt's bit for bit.  residual_f16 may be Y_f16
+ * itself (added in place), and may not overlap it otherwise.  Kernel choice as
+ * for fp8q_linear; of fp8q_set_gemm_tuning, tile_n = 512 is taken as 256.
+ */
+fp8q_status fp8q_linear_epilogue(const uint8_t* Xq, fp8q_format x_fmt, const float* s_x,
+                                 const uint8_t* Wq, const float* s_w,
+                                 int64_t M, int64_t N, int64_t K,
+                                 const void* bias_f16, fp8q_activation activation,
+                                 const void* residual_f16, void* Y_f16, void* stream);
+
+/*
+ * MoE router.  logits_f16 [T,E] fp16 (the gate's output) in; out:
+ *   experts    int32 [T,topk]  the topk largest logits of each token, largest
+ *                              first, ties to the lower expert;
+ *   weights    fp32  [T,topk]  softmax over the chosen logits (renormalize
+ *                              != 0) or over all E logits (renormalize == 0);
+ *   offsets    int32 [E+1]     rows grouped by (expert, token): rows
+ *                              offsets[e] .. offsets[e+1]-1 are expert e's;
+ *   row_token  int32 [T*topk]  token of each grouped row;
+ *   row_weight fp32  [T*topk]  its weight;
+ *   token_rows int32 [T,topk]  grouped row of each (token, choice):
+ * the inputs of fp8q_quantize_rows_dispatch, fp8q_moe_grouped_linear[_gather,
+ * _combine] and fp8q_moe_layer.  Logits may be infinite or NaN: NaN ranks below
+ * -inf, both weigh 0 (a choice among them happens only when fewer than topk
+ * logits are larger); a token without any logit above -inf gets weights 0, and
+ * +inf logits share the token's weight equally.  1 <= topk <= min(8, E), E <=
+ * 1024, T <= 2^22; T == 0 writes offsets (zeros) only.  workspace: int32
+ * [fp8q_moe_route_workspace_words(T, E)], device, need not be initialized, may be
+ * NULL when that is 0; calls whose work overlaps on the GPU need one each.
+ */
+fp8q_status fp8q_moe_route(const void* logits_f16, int64_t T, int32_t E, int32_t topk, int renormalize,
+                           int32_t* experts, float* weights, int32_t* offsets, int32_t* row_token,
+                           float* row_weight, int32_t* token_rows, int32_t* workspace, void* stream);
+
+/* int32 words of fp8q_moe_route's workspace (0 up to 64 tokens). */
+int64_t fp8q_moe_route_workspace_words(int64_t T, int32_t E);
+
+/*
+ * A whole MoE FFN for a few tokens, from the fp16 token matrix and the router's
+ * choices back to it:
+ *   per (token t, choice j) with e = experts[t,j]:
+ *     z = ((X_q[t] . Wq_up[e]^T) * s_x[t]) * s_up[e]
+ *     h = fp16(act(z)),  gated != 0: fp16(act(z[0:F]) * z[F:2F])
+ *     y = ((h_q . Wq_down[e]^T) * s_h) * s_down[e]
+ *   out[t] = fp16(sum_j weights[t,j] * y[t,j] + residual[t])
+ * X_q, s_x and h_q, s_h: the E4M3 codes and scales of
+ * fp8q_quantize_rows_dynamic.  Sums in fp32; h and out are rounded once each.
+ *   X_f16 [T,K], experts int32 [T,topk] (-1: no expert, adds nothing -- a
+ *   padded token has -1 throughout and gets its residual, or zero), weights
+ *   fp32 [T,topk] (not read where the expert is -1), Wq_up uint8 [E,F,K] or,
+ *   gated, [E,2F,K] (the activated rows first) with s_up fp32 [E,F] / [E,2F],
+ *   Wq_down uint8 [E,N,F] with s_down fp32 [E,N], residual_f16 [T,N] or NULL
+ *   (may be out_f16 itself, may not overlap it otherwise), out_f16 [T,N].
+ * An expert outside [-1, E) sets FP8Q_DEVERR_BAD_OFFSETS and adds nothing.
+ * T <= FP8Q_MOE_LAYER_MAX_TOKENS (0: no-op); K and F multiples of 16 up to
+ * 8192, N a multiple of 8, topk <= 8, E <= 1024.  Larger batches are served by
+ * fp8q_moe_route and the grouped linears.  workspace:
+ * fp8q_moe_layer_workspace_bytes(...) bytes, device, need not be initialized;
+ * calls whose work overlaps on the GPU need one each.  The weights are static
+ * inputs as for the linears (see the top of this file).
+ */
+#define FP8Q_MOE_LAYER_MAX_TOKENS 128
+fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts, const float* weights,
+                           int32_t topk, int32_t E, const uint8_t* Wq_up, const float* s_up,
+                           const uint8_t* Wq_down, const float* s_down, int64_t K, int64_t F, int64_t N,
+                           fp8q_activation activation, int gated, const void* residual_f16,
+                           void* out_f16, void* workspace, void* stream);
+int64_t fp8q_moe_layer_workspace_bytes(int64_t T, int32_t topk, int64_t F, int64_t N);
+
 /*
  * Diagnostic: the device E4M3 cast on its own, out[i] = E4M3(x[i]) with the
  * same rounding as the quantizers (RNE, saturating to ±448).  n >= 0,

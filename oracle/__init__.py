@@ -30,8 +30,12 @@ from .e5m2 import E5M2_MAX, e5m2_decode, e5m2_encode
 from .quant import EPS, quant_blocks, quant_rows, quant_tensor
 from .linear import (linear_blockscaled_ref, linear_f64_unquantized, linear_ref, moe_blockscaled_ref, moe_combine_ref,
                      moe_gather_ref, moe_ref)
+from .ffn import (activation_ref, linear_epilogue_ref, moe_hidden_ref, moe_layer_ref, moe_out_ref, product_terms,
+                  route_ref)
 
 __all__ = ["E4M3_MAX", "e4m3_decode", "e4m3_encode", "E5M2_MAX", "e5m2_decode", "e5m2_encode",
            "EPS", "quant_rows", "quant_tensor", "quant_blocks", "linear_ref", "moe_ref",
            "linear_blockscaled_ref", "moe_blockscaled_ref", "moe_gather_ref", "moe_combine_ref",
-           "linear_f64_unquantized"]
+           "linear_f64_unquantized",
+           "activation_ref", "linear_epilogue_ref", "route_ref", "moe_hidden_ref", "moe_out_ref", "moe_layer_ref",
+           "product_terms"]
