@@ -692,27 +692,52 @@ cudaError_t launch_route(const RouteParams& p, int dev, cudaStream_t st) {
 // hidden rows fp16 [rows, F], then y fp32 [rows, N]
 int64_t moe_layer_y_offset(int64_t rows, int64_t F) { return (rows * F * 2 + 255) & ~int64_t(255); }
 
-template <int NT, int kDepth, bool kUp, bool kGated>
-fp8q_status launch_moe_few(MoeFewParams p, int dev, int sms, cudaStream_t st) {
-  const MoeFewLayout l = mf_layout(NT, kDepth, p.K, 8, p.rows, p.E);
-  const int fit = (kMfMaxSmem - l.total) / l.pitch / 8 * 8;
-  if (fit < 8) return invalid("fp8q_moe_layer: a row does not fit in shared memory");   // (K, F <= 8192 always fit)
+template <int NT, bool kUp, bool kGated>
+fp8q_status launch_moe_few(const uint8_t* W, MoeFewParams p, int dev, int sms, cudaStream_t st) {
+  constexpr int kHalves = kUp && kGated ? 2 : 1;
+  // The widest units that leave a CTA at least three, so that equal shares differ
+  // little (experts: at most one a row).
+  const int64_t experts = p.rows < p.E ? p.rows : p.E;
+  auto share = [&](int ru) {
+    const int outs = ru / kHalves;
+    return (experts * ((p.n_out + outs - 1) / outs) + sms - 1) / sms;
+  };
+  p.ru = share(64) >= 3 ? 64 : share(32) >= 3 || kHalves == 2 ? 32 : 16;
+  // Segments of up to NT * 8 rows, fewer if they leave the ring under two stages;
+  // the ring takes the rest, up to what a CTA's share can fill.
+  const MoeFewLayout l = mf_layout(NT, p.K, 8, 2, p.rows, p.E);
+  const int room = kMfMaxSmem - l.total;   // for rows beyond the first eight
+  if (room < 0) return invalid("fp8q_moe_layer: a row does not fit in shared memory");   // (K, F <= 8192 always fit)
+  const int fit = 8 + room / l.pitch / 8 * 8;
   p.rmax = fit < NT * 8 ? fit : NT * 8;
-  const size_t smem = size_t(l.total) + size_t(p.rmax) * l.pitch;
-  cudaError_t e = ensure_smem<moe_few_kernel<NT, kDepth, kUp, kGated>>(kMfMaxSmem, dev);
+  const int base = mf_layout(NT, p.K, p.rmax, 0, p.rows, p.E).total;
+  const int64_t fill = share(p.ru) * ((p.K + 256 * (128 / p.ru) - 1) / (256 * (128 / p.ru)));
+  int stages = (kMfMaxSmem - base) / kMfStageBytes;
+  if (stages > kMfMaxStages) stages = kMfMaxStages;
+  if (stages > fill) stages = fill < 2 ? 2 : static_cast<int>(fill);
+  p.stages = stages;
+  CUtensorMap tw;
+  const fp8q_status s = make_operand_map(&tw, W, int64_t(p.E) * kHalves * p.n_out, p.K, p.ru / kHalves);
+  if (s != FP8Q_OK) return s;
+  cudaError_t e = ensure_smem<moe_few_kernel<NT, kUp, kGated>>(kMfMaxSmem, dev);
   if (e == cudaSuccess)
-    e = launch_ex(moe_few_kernel<NT, kDepth, kUp, kGated>, dim3(sms), dim3(kMfThreads), smem, st, 1, true, p);
+    e = launch_ex(moe_few_kernel<NT, kUp, kGated>, dim3(sms), dim3(kMfThreads), size_t(base) + stages * kMfStageBytes,
+                  st, 1, true, tw, p);
   if (e != cudaSuccess) return cuda_fail(e, "moe_few_kernel launch");
   return FP8Q_OK;
 }
 
-// n-tiles by the batch: an expert sees at most T rows (one a token).
+// n-tiles by the rows of an expert, twice the mean of an even choice (an expert
+// with more is cut into segments, whose weights then come from L2), and at
+// most the tokens.
 template <bool kUp, bool kGated>
-fp8q_status launch_moe_few_nt(const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
-  if (T <= 8) return launch_moe_few<1, 6, kUp, kGated>(p, dev, sms, st);
-  if (T <= 16) return launch_moe_few<2, 6, kUp, kGated>(p, dev, sms, st);
-  if (T <= 32) return launch_moe_few<4, 6, kUp, kGated>(p, dev, sms, st);
-  return launch_moe_few<8, 4, kUp, kGated>(p, dev, sms, st);
+fp8q_status launch_moe_few_nt(const uint8_t* W, const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
+  const int64_t mean2 = (2 * int64_t(p.rows) + p.E - 1) / p.E;
+  const int64_t rows = mean2 < T ? mean2 : T;
+  if (rows <= 8) return launch_moe_few<1, kUp, kGated>(W, p, dev, sms, st);
+  if (rows <= 16) return launch_moe_few<2, kUp, kGated>(W, p, dev, sms, st);
+  if (rows <= 32) return launch_moe_few<4, kUp, kGated>(W, p, dev, sms, st);
+  return launch_moe_few<8, kUp, kGated>(W, p, dev, sms, st);
 }
 
 }  // namespace
@@ -1171,6 +1196,7 @@ fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts,
   if (K <= 0 || K > 8192 || K % 16 != 0) return invalid("K must be a positive multiple of 16, at most 8192");
   if (F <= 0 || F > 8192 || F % 16 != 0) return invalid("F must be a positive multiple of 16, at most 8192");
   if (N <= 0 || N > (1 << 20) || N % 8 != 0) return invalid("N must be a positive multiple of 8, at most 2^20");
+  if (int64_t(E) * N > kMaxDim) return invalid("E*N must be below 2^31");
   if (T == 0) return FP8Q_OK;
   if (!aligned16(X_f16) || !aligned16(Wq_up) || !aligned16(s_up) || !aligned16(Wq_down) || !aligned16(s_down) ||
       !aligned16(out_f16) || !aligned16(workspace))
@@ -1190,7 +1216,6 @@ fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts,
   MoeFewParams p = {};
   p.x = static_cast<const __half*>(X_f16);
   p.experts = experts;
-  p.w = Wq_up;
   p.s_w = s_up;
   p.rows = static_cast<int>(rows);
   p.topk = topk;
@@ -1200,15 +1225,14 @@ fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts,
   p.act = activation;
   p.hidden = static_cast<__half*>(workspace);
   p.y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + moe_layer_y_offset(rows, F));
-  fp8q_status s = gated ? launch_moe_few_nt<true, true>(p, T, dev, sms, st)
-                        : launch_moe_few_nt<true, false>(p, T, dev, sms, st);
+  fp8q_status s = gated ? launch_moe_few_nt<true, true>(Wq_up, p, T, dev, sms, st)
+                        : launch_moe_few_nt<true, false>(Wq_up, p, T, dev, sms, st);
   if (s != FP8Q_OK) return s;
   p.x = p.hidden;
-  p.w = Wq_down;
   p.s_w = s_down;
   p.K = static_cast<int>(F);
   p.n_out = static_cast<int>(N);
-  s = launch_moe_few_nt<false, false>(p, T, dev, sms, st);
+  s = launch_moe_few_nt<false, false>(Wq_down, p, T, dev, sms, st);
   if (s != FP8Q_OK) return s;
   const int64_t items = T * (N >> 2);
   const int grid = static_cast<int>(items < 256 * int64_t(sms) ? (items + 255) / 256 : sms);

@@ -22,36 +22,40 @@
 // 1.7 us and more for K = 2048 on the one chain, where here eight warps share K.
 //
 // Work: the chosen experts, each cut into segments of at most rmax rows; a segment
-// is a run of blocks of 16 outputs.  Every CTA takes an equal share of
-// the blocks of all segments.  For a segment it first quantizes the rows into
-// shared memory; its warps then take blocks, S of them sharing a block's K
-// (S by cost, per CTA).  A lane copies the 16-byte pieces of weight rows that its
-// own MMA fragments need with cp.async into a private ring, kDepth pieces of 16
-// rows x 128 bytes ahead across block and segment boundaries, so the
-// copies need no barrier.  K may be permuted in a product as long as both
-// operands agree: lane (g, t) holds bytes 16 t .. 16 t + 15 of a 64-byte group of
-// row g, which is one 16-byte load per row for two MMAs, for both operands.
-// The S partial sums of a block meet in shared memory and are added in fixed order.
+// is a run of units of `outs` outputs (RU = 16, 32 or 64 weight rows; gated: half of
+// them from each half of the up projection).  Every CTA takes an equal share of
+// the units of all segments.  One warp streams the weights with TMA (boxes of 128
+// bytes of K x the unit's rows, 128-byte swizzle) through a ring of 32 KB stages, as
+// far ahead of eight consumer warps as the ring reaches, across unit and segment
+// boundaries.  For a segment the consumers first quantize its rows into shared
+// memory; then S = 128 / RU of them share a 16-row tile's K, 256 bytes each a stage.
+// K may be permuted in a product as long as both operands agree: lane (g, t) holds
+// bytes 16 t .. 16 t + 15 of a 64-byte group of row g, which is one 16-byte shared
+// load per row for two MMAs, for both operands.  The S partial sums of a tile
+// meet in shared memory and are added in fixed order.
 #pragma once
+
+#include <cuda.h>
 
 #include "activation.cuh"
 #include "quant_rows.cuh"
 
 namespace fp8q {
 
-constexpr int kMfThreads = 256;
-constexpr int kMfWarps = kMfThreads / 32;
+constexpr int kMfWarps = 8;                          // consumer warps
+constexpr int kMfConsumers = kMfWarps * 32;
+constexpr int kMfThreads = kMfConsumers + 32;        // + the warp that streams the weights
 constexpr int kMfMaxRows = 1024;       // T * topk
 constexpr int kMfMaxTopk = 8;
 constexpr int kMfMaxExperts = 1024;
-constexpr int kMfChunk = 128;          // K bytes of a ring piece
-constexpr int kMfPieceBytes = 16 * kMfChunk;
+constexpr int kMfWarpK = 256;          // K bytes a warp takes of a stage
+constexpr int kMfStageBytes = 32768;   // RU weight rows x 256 S bytes, S = 128 / RU
+constexpr int kMfMaxStages = 6;
 constexpr int kMfMaxSmem = 232448;     // 227 KB
 
 struct MoeFewParams {
   const __half* x;          // up: [T, K]; down: hidden [T * topk, K]
   const int32_t* experts;   // [T * topk], -1: none
-  const uint8_t* w;         // [E, wrows, K] E4M3
   const float* s_w;         // [E, wrows]
   int rows;                 // T * topk
   int topk;
@@ -62,30 +66,34 @@ struct MoeFewParams {
   __half* hidden;           // up: [T * topk, F]
   float* y;                 // down: [T * topk, N]
   int rmax;                 // rows of a segment, a multiple of 8
+  int ru;                   // weight rows of a unit: 16, 32 or 64 (gated: 32 or 64)
+  int stages;               // of the ring
 };
 
 // Shared-memory layout, the same on host and device.
 struct MoeFewLayout {
-  int pitch;      // bytes of a row of codes; 64 mod 128 keeps even and odd rows on different banks
-  int ring;       // offsets
+  int pitch;      // bytes of a row of codes
+  int codes;      // offsets
   int part;
+  int scales;
+  int bars;
   int rows;
   int segs;
   int counts;
-  int scales;
   int total;
 };
 __host__ __device__ constexpr int mf_part_units(int nt) { return nt >= 4 ? 8 : 2 * nt; }   // x 4 KB
-__host__ __device__ inline MoeFewLayout mf_layout(int nt, int depth, int K, int rmax, int R, int E) {
+__host__ __device__ inline MoeFewLayout mf_layout(int nt, int K, int rmax, int stages, int R, int E) {
   MoeFewLayout l;
-  l.pitch = (K + kMfChunk - 1) / kMfChunk * kMfChunk + 64;
-  l.ring = 0;
-  l.part = kMfWarps * depth * kMfPieceBytes;
+  l.pitch = (K + 127) / 128 * 128 + 64;
+  l.codes = stages * kMfStageBytes;                    // the ring comes first (swizzle atoms: 1 KB aligned)
+  l.part = l.codes + rmax * l.pitch;
   l.scales = l.part + mf_part_units(nt) * kMfWarps * 512;
-  l.rows = l.scales + 64 * 4;
+  l.bars = l.scales + (64 + kMfWarps) * 4;             // row scales, then the build's partial maxima
+  l.rows = l.bars + (2 * kMfMaxStages + 1) * 8;        // full, empty; the last word: abort flag
   l.segs = l.rows + R * 4;
   l.counts = l.segs + R * 4;
-  l.total = (l.counts + (E + 4) * 4 + 15) & ~15;   // then the codes: rmax * pitch
+  l.total = l.counts + (E + 4) * 4;
   return l;
 }
 
@@ -166,52 +174,83 @@ __device__ __forceinline__ int mf_schedule(const MoeFewParams& p, int* rows, int
   return counts[p.E];
 }
 
-// Quantize the rows of a segment into shared memory (codes [cnt][pitch], zero
-// behind K up to the pitch's last chunk; scales).  One warp per row.
+// Consumer warps: quantize the rows of a segment into shared memory (codes
+// [cnt][pitch], zero behind K; scales).  With few rows several warps share one
+// (their maxima meet in `maxima`), so that a row's loads are all in flight at once.
 template <bool kUp>
 __device__ __forceinline__ void mf_build_rows(const MoeFewParams& p, int seg, const int* rows, uint8_t* codes,
-                                              int pitch, float* scales, int warp, int lane) {
+                                              int pitch, float* scales, float* maxima, int warp, int lane) {
+  constexpr int kHeld = 8;   // 16-byte vectors a lane keeps between the maximum and the codes
   const int cnt = mf_seg_count(seg), row0 = mf_seg_row0(seg);
+  const int share = cnt > 4 ? 1 : cnt > 2 ? 2 : cnt > 1 ? 4 : 8;   // warps of a row
   const int nvec = p.K >> 3;
-  const int nvec_pad = (p.K + kMfChunk - 1) / kMfChunk * (kMfChunk / 8);
-  for (int i = warp; i < cnt; i += kMfWarps) {
-    const int slot = rows[row0 + i];
-    const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(kUp ? slot / p.topk : slot) * p.K);
+  const int nvec_pad = (pitch - 64) >> 3;
+  const int j0 = (warp % share) * 32 + lane, step = share * 32;
+  for (int i0 = 0; i0 < cnt; i0 += kMfWarps / share) {
+    const int i = i0 + warp / share;
+    const bool live = i < cnt;
+    const uint4* src = nullptr;
+    uint4 v[kHeld];
     float m = 0.0f;
-    for (int j = lane; j < nvec; j += 32) m = absmax8(src[j], m);
+    if (live) {
+      const int slot = rows[row0 + i];
+      src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(kUp ? slot / p.topk : slot) * p.K);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const RowScale rs = row_scale_from_amax(m);
-    uint2* dst = reinterpret_cast<uint2*>(codes + i * pitch);
-    for (int j = lane; j < nvec_pad; j += 32) dst[j] = j < nvec ? encode8(src[j], rs.r) : make_uint2(0u, 0u);
-    if (lane == 0) scales[i] = rs.s;
+      for (int u = 0; u < kHeld; ++u)
+        v[u] = j0 + u * step < nvec ? ld_global_v4(src + j0 + u * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) m = absmax8(v[u], m);
+      for (int j = j0 + kHeld * step; j < nvec; j += step) m = absmax8(ld_global_v4(src + j), m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    if (share > 1) {   // uniform; one pass over the rows in this case
+      if (lane == 0) maxima[warp] = m;
+      named_barrier(1, kMfConsumers);
+      for (int k = 0; k < share; ++k) m = fmaxf(m, maxima[warp / share * share + k]);
+    }
+    if (live) {
+      const RowScale rs = row_scale_from_amax(m);
+      uint2* dst = reinterpret_cast<uint2*>(codes + i * pitch);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)   // (vectors behind K are zero: zero codes)
+        if (j0 + u * step < nvec_pad) dst[j0 + u * step] = encode8(v[u], rs.r);
+      for (int j = j0 + kHeld * step; j < nvec_pad; j += step)
+        dst[j] = j < nvec ? encode8(ld_global_v4(src + j), rs.r) : make_uint2(0u, 0u);
+      if (j0 == 0) scales[i] = rs.s;
+    }
   }
 }
 
-// Where a warp stands in its CTA's share: segment, first block of the round, chunk.
-struct MfIter {
-  int seg;
-  int end;    // last block of the segment in this share, exclusive
-  int base;   // first block of the round
-  int c;      // next chunk of K
-};
-
-// NT: n-tiles of 8 rows a segment may have; kDepth: ring pieces per warp.
-template <int NT, int kDepth, bool kUp, bool kGated>
-__global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const MoeFewParams p) {
-  extern __shared__ __align__(128) uint8_t mf_smem[];
-  constexpr int kTiles = kUp && kGated ? 2 : 1;   // 16-row weight tiles of a block of 16 outputs
+// NT: n-tiles of 8 rows a segment may have.  tmW: the weights [E * wrows, K] in
+// boxes of 128 bytes x RU rows (gated: RU / 2).
+template <int NT, bool kUp, bool kGated>
+__global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                             const MoeFewParams p) {
+  extern __shared__ __align__(1024) uint8_t mf_smem[];
+  constexpr int kHalves = kUp && kGated ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t4 = lane & 3;
-  const MoeFewLayout L = mf_layout(NT, kDepth, p.K, p.rmax, p.rows, p.E);
-  uint8_t* ring = mf_smem + L.ring + warp * kDepth * kMfPieceBytes;
+  const MoeFewLayout L = mf_layout(NT, p.K, p.rmax, p.stages, p.rows, p.E);
+  uint8_t* ring = mf_smem;
+  uint8_t* codes = mf_smem + L.codes;
   float* part = reinterpret_cast<float*>(mf_smem + L.part);
   float* scales = reinterpret_cast<float*>(mf_smem + L.scales);
+  uint64_t* full = reinterpret_cast<uint64_t*>(mf_smem + L.bars);
+  uint64_t* empty = full + kMfMaxStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + kMfMaxStages);
   int* rows = reinterpret_cast<int*>(mf_smem + L.rows);
   int* segs = reinterpret_cast<int*>(mf_smem + L.segs);
   int* counts = reinterpret_cast<int*>(mf_smem + L.counts);
-  uint8_t* codes = mf_smem + L.total;
 
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMfMaxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kMfWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmW);
+  }
   // The experts may come from the kernel just before the up projection.  The
   // down projection starts once every CTA of the up projection has passed this
   // wait, so the experts are there and only the hidden rows are waited for.
@@ -220,170 +259,154 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const MoeFewParams 
     pdl_launch_dependents();
   }
   const int nseg = mf_schedule(p, rows, segs, counts, reinterpret_cast<int*>(part), kUp && blockIdx.x == 0);
-  const int nb = (p.n_out + 15) / 16;
-  const int total = nseg * nb;
+  const int outs = p.ru / kHalves;                  // outputs of a unit
+  const int nu = (p.n_out + outs - 1) / outs;       // units of a segment
+  const int total = nseg * nu;
   const int lo = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
   const int hi = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+  const int S = 128 / p.ru;                         // warps that share a tile's K
+  const int boxes = (p.K + 127) / 128;              // 128-byte boxes of K
+  const int stage_boxes = 2 * S;
+  const int wrows = kHalves * p.n_out;
 
-  // S warps share a block's K: the cheapest in chunks a warp walks through.
-  const int nc = (p.K + kMfChunk - 1) / kMfChunk;
-  int S = 1, cost = 1 << 30;
+  if (warp == kMfWarps) {
+    // ------------------------------------------------------------ weights
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t ph = 0, armed = 0, armed_ph = 0;
+      bool ok = true;
+      int s = lo < hi ? lo / nu : 0;
+      int n0 = (lo - s * nu) * outs;
+      for (int i = lo; i < hi && ok; ++i) {
+        const int row = mf_seg_expert(segs[s]) * wrows + n0;
+        for (int b0 = 0; b0 < boxes; b0 += stage_boxes) {
+          const int nbox = min(stage_boxes, boxes - b0);
+          if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(nbox * p.ru * 128));
+          uint8_t* dst = ring + slot * kMfStageBytes;
+          for (int b = 0; b < nbox; ++b) {
 #pragma unroll
-  for (int s = 1; s <= kMfWarps / kTiles; s *= 2) {
-    const int per_round = kMfWarps / (s * kTiles);
-    const int c = ((hi - lo + per_round - 1) / per_round) * ((nc + s - 1) / s);
-    if (s <= nc && c < cost) {
-      cost = c;
-      S = s;
-    }
-  }
-  const int per_round = kMfWarps / (S * kTiles);   // blocks of a round
-  const int ks = warp % S, tl = warp / S;
-  const int my_block = tl / kTiles, sub = tl % kTiles;
-  const int c0 = ks * nc / S, c1 = (ks + 1) * nc / S;
-  const int wrows = kTiles * p.n_out;
-
-  // First position at or after segment s; (seg, base) with base >= hi: the end.
-  auto enter = [&](MfIter& it, int s) {
-    it.seg = s;
-    it.base = max(lo, s * nb);
-    it.end = min(hi, (s + 1) * nb);
-    it.c = c0;
-  };
-  // Next item.  A warp without a block in a round has one empty item there.
-  auto step = [&](MfIter& it) -> bool {   // true: the round ended
-    if (it.base + my_block < it.end && ++it.c < c1) return false;
-    it.base += per_round;
-    it.c = c0;
-    if (it.base >= it.end && it.end < hi) enter(it, it.seg + 1);
-    return true;
-  };
-
-  MfIter ld;
-  const uint8_t* wptr = nullptr;   // this lane's first byte of row g of the loader's tile
-  bool ok_lo = false, ok_hi = false;
-  auto set_tile = [&]() {
-    const int b = ld.base + my_block;
-    ok_lo = ok_hi = false;
-    if (ld.base < hi && b < ld.end) {
-      const int n0 = (b - ld.seg * nb) * 16 + g;   // this lane's output rows n0 and n0 + 8
-      ok_lo = n0 < p.n_out;
-      ok_hi = n0 + 8 < p.n_out;
-      wptr = p.w + (static_cast<int64_t>(mf_seg_expert(segs[ld.seg])) * wrows + sub * p.n_out + n0) * p.K + 16 * t4;
-    }
-  };
-  const uint32_t ring_lane = smem_u32(ring) + lane * 16;
-  auto issue = [&](int slot) {
-    if (ld.base < hi) {
-      const uint32_t dst = ring_lane + slot * kMfPieceBytes;
-      const int k = ld.c * kMfChunk + 16 * t4;
-      const bool k0 = k < p.K, k1 = k + 64 < p.K;
-      const uint8_t* src = wptr + ld.c * kMfChunk;
-      const uint8_t* src8 = src + static_cast<int64_t>(8) * p.K;
-      if (ok_lo) {   // (outputs past the end are neither loaded nor stored)
-        cp_async_16_zfill(dst, k0 ? src : p.w, k0 ? 16u : 0u);
-        cp_async_16_zfill(dst + 1024, k1 ? src + 64 : p.w, k1 ? 16u : 0u);
+            for (int q = 0; q < kHalves; ++q) {
+              tma_load_2d(dst, &tmW, &full[slot], (b0 + b) * 128, row + q * p.n_out);
+              dst += outs * 128;
+            }
+          }
+          armed |= 1u << slot;
+          armed_ph = (armed_ph & ~(1u << slot)) | (ph << slot);
+          if (++slot == p.stages) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        }
+        n0 += outs;
+        if (n0 >= p.n_out) {
+          n0 = 0;
+          ++s;
+        }
       }
-      if (ok_hi) {
-        cp_async_16_zfill(dst + 512, k0 ? src8 : p.w, k0 ? 16u : 0u);
-        cp_async_16_zfill(dst + 1536, k1 ? src8 + 64 : p.w, k1 ? 16u : 0u);
+      if (!ok) {
+        raise_error(0x1u);
+        *abort_flag = 1;
       }
-      if (step(ld)) set_tile();
+      // No copy may still be in flight when the CTA exits.
+      for (int i = 0; i < p.stages; ++i)
+        if (armed & (1u << i)) mbar_wait(&full[i], (armed_ph >> i) & 1u, nullptr);
     }
-    cp_async_commit();
-  };
-  int slot_ld = 0, slot = 0;
-  if (lo < hi) {
-    enter(ld, lo / nb);
-    set_tile();
-  } else {
-    ld.base = hi;
+    return;
   }
-#pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) issue(slot_ld++);
-  slot_ld = kDepth - 1;
 
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, t4 = lane & 3;
+  const int ks = warp % S, tl = warp / S;           // share of K, 16-row tile of the unit
   if (!kUp) {
     pdl_wait_prior_grid();
     pdl_launch_dependents();
   }
-
-  MfIter it;
-  if (lo < hi) enter(it, lo / nb);
-  int buf = 0;
-  for (int s = lo < hi ? lo / nb : nseg; s * nb < hi; ++s) {
+  int slot = 0, buf = 0;
+  uint32_t ph = 0;
+  for (int s = lo < hi ? lo / nu : nseg; s * nu < hi; ++s) {
     const int seg = segs[s];
-    const int cnt = mf_seg_count(seg);
+    const int e = mf_seg_expert(seg), cnt = mf_seg_count(seg), row0 = mf_seg_row0(seg);
     const int nt = (cnt + 7) >> 3;
-    const int units = mf_part_units(NT);
-    const bool two = 2 * nt <= units;   // two partial buffers fit: one barrier a round
-    __syncthreads();                    // the codes and partials of the segment before are done with
-    mf_build_rows<kUp>(p, seg, rows, codes, L.pitch, scales, warp, lane);
-    __syncthreads();
-    const uint8_t* brow = codes + g * L.pitch + 16 * t4;
-    const int base0 = it.base, end = it.end;
-    for (int base = base0; base < end; base += per_round) {
-      const bool mine = base + my_block < end;
+    const bool two = 2 * nt <= mf_part_units(NT);   // two partial buffers fit: one barrier a unit
+    named_barrier(1, kMfConsumers);                 // the codes and partials of the segment before are done with
+    mf_build_rows<kUp>(p, seg, rows, codes, L.pitch, scales, scales + 64, warp, lane);
+    named_barrier(1, kMfConsumers);
+    const uint32_t brow = smem_u32(codes + g * L.pitch + 16 * t4);
+    const int first = max(lo, s * nu), end = min(hi, (s + 1) * nu);
+    for (int unit = first; unit < end; ++unit) {
+      const int n0 = (unit - s * nu) * outs;
+      // the weight scales of this thread's first output, in flight during the mainloop
+      const int u = threadIdx.x & (outs - 1), r1 = threadIdx.x / outs;
+      const float* sw = p.s_w + static_cast<int64_t>(e) * wrows + n0 + u;
+      const bool live = n0 + u < p.n_out;
+      float w[kHalves];
+#pragma unroll
+      for (int q = 0; q < kHalves; ++q) w[q] = live ? __ldg(sw + q * p.n_out) : 0.0f;
       float acc[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-      for (int c = c0; c < (mine ? c1 : c0 + 1); ++c) {
-        cp_async_wait_group<kDepth - 2>();
-        if (mine) {
-          const uint32_t src = ring_lane + slot * kMfPieceBytes;
-          const uint4 l0 = ld_shared_v4(src), h0 = ld_shared_v4(src + 512);
-          const uint4 l1 = ld_shared_v4(src + 1024), h1 = ld_shared_v4(src + 1536);
-          const uint32_t b0 = smem_u32(brow + c * kMfChunk);
+      for (int b0 = 0; b0 < boxes; b0 += stage_boxes) {
+        if (!mbar_wait(&full[slot], ph, abort_flag)) {
+          // give up, but walk on: every warp meets the same barriers
+          if (lane == 0) raise_error(0x4u);
+          *abort_flag = 1;
+        }
+        const uint32_t arow = smem_u32(ring + slot * kMfStageBytes) + (tl * 16 + g) * 128;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if (j < nt) {
-              const uint4 v0 = ld_shared_v4(b0 + j * 8 * L.pitch);
-              mma_e4m3_m16n8k32(acc[j], l0.x, h0.x, l0.y, h0.y, v0.x, v0.y);
-              mma_e4m3_m16n8k32(acc[j], l0.z, h0.z, l0.w, h0.w, v0.z, v0.w);
-              const uint4 v1 = ld_shared_v4(b0 + j * 8 * L.pitch + 64);
-              mma_e4m3_m16n8k32(acc[j], l1.x, h1.x, l1.y, h1.y, v1.x, v1.y);
-              mma_e4m3_m16n8k32(acc[j], l1.z, h1.z, l1.w, h1.w, v1.z, v1.w);
+        for (int h = 0; h < 4; ++h) {   // 64-byte groups of this warp's two boxes
+          const int box = 2 * ks + (h >> 1);
+          if (b0 + box < boxes) {
+            // 16-byte chunk c of a row lies at chunk c ^ (row & 7)
+            const uint32_t at = arow + box * p.ru * 128 + ((((h & 1) * 4 + t4) ^ g) << 4);
+            const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 8 * 128);
+            const uint32_t xrow = brow + (b0 + box) * 128 + (h & 1) * 64;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if (j < nt) {
+                const uint4 x = ld_shared_v4(xrow + j * 8 * L.pitch);
+                mma_e4m3_m16n8k32(acc[j], a.x, b.x, a.y, b.y, x.x, x.y);
+                mma_e4m3_m16n8k32(acc[j], a.z, b.z, a.w, b.w, x.z, x.w);
+              }
             }
           }
         }
-        issue(slot_ld);
-        if (++slot == kDepth) slot = 0;
-        if (++slot_ld == kDepth) slot_ld = 0;
-      }
-      // partial sums of the round, then the outputs
-      float* pb = part + (two ? buf : 0) * nt * kMfWarps * 128;
-      if (!two && base != base0) __syncthreads();   // the round before has been read
-      if (mine) {
-        float* dst = pb + warp * nt * 128 + g * 8 + 2 * t4;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j < nt) {
-            *reinterpret_cast<float2*>(dst + j * 128) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2*>(dst + j * 128 + 64) = make_float2(acc[j][2], acc[j][3]);
-          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (++slot == p.stages) {
+          slot = 0;
+          ph ^= 1u;
         }
       }
-      __syncthreads();
-      const int e = mf_seg_expert(seg), row0 = mf_seg_row0(seg);
-      const int blocks = min(per_round, end - base);
-      for (int i = threadIdx.x; i < blocks * cnt * 16; i += kMfThreads) {
-        const int u = i & 15, br = i >> 4;
-        const int r = br % cnt, b = br / cnt;
-        const int n = (base + b - s * nb) * 16 + u;
-        if (n >= p.n_out) continue;
-        float z[kTiles];
+      // partial sums of the unit, then its outputs
+      float* pb = part + (two ? buf : 0) * nt * kMfWarps * 128;
+      if (!two && unit != first) named_barrier(1, kMfConsumers);   // the unit before has been read
+      float* dst = pb + warp * nt * 128 + g * 8 + 2 * t4;
 #pragma unroll
-        for (int q = 0; q < kTiles; ++q) {
-          const float* src = pb + (b * kTiles + q) * S * nt * 128 + (r >> 3) * 128 + u * 8 + (r & 7);
+      for (int j = 0; j < NT; ++j) {
+        if (j < nt) {
+          *reinterpret_cast<float2*>(dst + j * 128) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(dst + j * 128 + 64) = make_float2(acc[j][2], acc[j][3]);
+        }
+      }
+      named_barrier(1, kMfConsumers);
+      for (int r = r1; r < cnt && live; r += kMfConsumers / outs) {
+        float z[kHalves];
+#pragma unroll
+        for (int q = 0; q < kHalves; ++q) {
+          const int tile = q * (outs / 16) + (u >> 4);
+          const float* src = pb + tile * S * nt * 128 + (r >> 3) * 128 + (u & 15) * 8 + (r & 7);
           float v = 0.0f;
           for (int k = 0; k < S; ++k) v = __fadd_rn(v, src[k * nt * 128]);
-          z[q] = __fmul_rn(__fmul_rn(v, scales[r]),
-                           __ldg(p.s_w + static_cast<int64_t>(e) * wrows + q * p.n_out + n));
+          z[q] = __fmul_rn(__fmul_rn(v, scales[r]), w[q]);
         }
-        const int64_t at = static_cast<int64_t>(rows[row0 + r]) * p.n_out + n;
+        const int64_t at = static_cast<int64_t>(rows[row0 + r]) * p.n_out + n0 + u;
         if (kUp) {
           float h = activate(z[0], p.act);
-          if (kGated) h = __fmul_rn(h, z[kTiles - 1]);
+          if (kGated) h = __fmul_rn(h, z[kHalves - 1]);
           p.hidden[at] = __float2half_rn(h);
         } else {
           p.y[at] = z[0];
@@ -391,9 +414,7 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const MoeFewParams 
       }
       buf ^= 1;
     }
-    if (end < hi) enter(it, s + 1);
   }
-  cp_async_wait_group<0>();
 }
 
 // out[t] = fp16(sum over the token's experts of weight * y + residual).
