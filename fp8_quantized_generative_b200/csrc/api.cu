@@ -692,52 +692,72 @@ cudaError_t launch_route(const RouteParams& p, int dev, cudaStream_t st) {
 // hidden rows fp16 [rows, F], then y fp32 [rows, N]
 int64_t moe_layer_y_offset(int64_t rows, int64_t F) { return (rows * F * 2 + 255) & ~int64_t(255); }
 
-template <int NT, bool kUp, bool kGated>
+// Units of a CTA's equal share when a unit has `outs` outputs (an expert to a row
+// at most).
+int64_t moe_few_share(const MoeFewParams& p, int outs, int sms) {
+  const int64_t experts = p.rows < p.E ? p.rows : p.E;
+  return (experts * ((p.n_out + outs - 1) / outs) + sms - 1) / sms;
+}
+
+template <int NT, int MT, bool kUp, bool kGated>
 fp8q_status launch_moe_few(const uint8_t* W, MoeFewParams p, int dev, int sms, cudaStream_t st) {
   constexpr int kHalves = kUp && kGated ? 2 : 1;
-  // The widest units that leave a CTA at least three, so that equal shares differ
-  // little (experts: at most one a row).
-  const int64_t experts = p.rows < p.E ? p.rows : p.E;
-  auto share = [&](int ru) {
-    const int outs = ru / kHalves;
-    return (experts * ((p.n_out + outs - 1) / outs) + sms - 1) / sms;
-  };
-  p.ru = share(64) >= 3 ? 64 : share(32) >= 3 || kHalves == 2 ? 32 : 16;
+  constexpr int kOuts = 16 * MT / kHalves;
+  p.units = static_cast<int>((p.n_out + kOuts - 1) / kOuts);
   // Segments of up to NT * 8 rows, fewer if they leave the ring under two stages;
   // the ring takes the rest, up to what a CTA's share can fill.
-  const MoeFewLayout l = mf_layout(NT, p.K, 8, 2, p.rows, p.E);
+  const MoeFewLayout l = mf_layout(NT, MT, p.K, 8, 2, p.rows, p.E);
   const int room = kMfMaxSmem - l.total;   // for rows beyond the first eight
   if (room < 0) return invalid("fp8q_moe_layer: a row does not fit in shared memory");   // (K, F <= 8192 always fit)
   const int fit = 8 + room / l.pitch / 8 * 8;
   p.rmax = fit < NT * 8 ? fit : NT * 8;
-  const int base = mf_layout(NT, p.K, p.rmax, 0, p.rows, p.E).total;
-  const int64_t fill = share(p.ru) * ((p.K + 256 * (128 / p.ru) - 1) / (256 * (128 / p.ru)));
+  const int base = mf_layout(NT, MT, p.K, p.rmax, 0, p.rows, p.E).total;
+  const int64_t fill = moe_few_share(p, kOuts, sms) * ((int64_t(p.K) * 16 * MT + kMfStageBytes - 1) / kMfStageBytes);
   int stages = (kMfMaxSmem - base) / kMfStageBytes;
   if (stages > kMfMaxStages) stages = kMfMaxStages;
   if (stages > fill) stages = fill < 2 ? 2 : static_cast<int>(fill);
   p.stages = stages;
   CUtensorMap tw;
-  const fp8q_status s = make_operand_map(&tw, W, int64_t(p.E) * kHalves * p.n_out, p.K, p.ru / kHalves);
+  const fp8q_status s = make_operand_map(&tw, W, int64_t(p.E) * kHalves * p.n_out, p.K, kOuts);
   if (s != FP8Q_OK) return s;
-  cudaError_t e = ensure_smem<moe_few_kernel<NT, kUp, kGated>>(kMfMaxSmem, dev);
+  cudaError_t e = ensure_smem<moe_few_kernel<NT, MT, kUp, kGated>>(kMfMaxSmem, dev);
   if (e == cudaSuccess)
-    e = launch_ex(moe_few_kernel<NT, kUp, kGated>, dim3(sms), dim3(kMfThreads), size_t(base) + stages * kMfStageBytes,
-                  st, 1, true, tw, p);
+    e = launch_ex(moe_few_kernel<NT, MT, kUp, kGated>, dim3(sms), dim3(kMfThreads),
+                  size_t(base) + stages * kMfStageBytes, st, 1, true, tw, p);
   if (e != cudaSuccess) return cuda_fail(e, "moe_few_kernel launch");
   return FP8Q_OK;
 }
 
-// n-tiles by the rows of an expert, twice the mean of an even choice (an expert
-// with more is cut into segments, whose weights then come from L2), and at
-// most the tokens.
+// n-tiles: twice the mean rows of an expert under an even choice, at most the
+// tokens (an expert with more rows is cut into segments, whose weights then come
+// from L2), and at most what leaves the ring two stages.  Weight tiles of a unit: as
+// many as leave a CTA three units or more, so that equal shares differ little
+// (wider units reload the rows less often and leave fewer partial sums).
 template <bool kUp, bool kGated>
-fp8q_status launch_moe_few_nt(const uint8_t* W, const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
+fp8q_status launch_moe_few_any(const uint8_t* W, const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
+  constexpr int kHalves = kUp && kGated ? 2 : 1;
   const int64_t mean2 = (2 * int64_t(p.rows) + p.E - 1) / p.E;
-  const int64_t rows = mean2 < T ? mean2 : T;
-  if (rows <= 8) return launch_moe_few<1, kUp, kGated>(W, p, dev, sms, st);
-  if (rows <= 16) return launch_moe_few<2, kUp, kGated>(W, p, dev, sms, st);
-  if (rows <= 32) return launch_moe_few<4, kUp, kGated>(W, p, dev, sms, st);
-  return launch_moe_few<8, kUp, kGated>(W, p, dev, sms, st);
+  int64_t rows = mean2 < T ? mean2 : T;
+  const MoeFewLayout l = mf_layout(8, 1, p.K, 0, 2, p.rows, p.E);
+  const int64_t fit = (kMfMaxSmem - l.total) / l.pitch / 8 * 8;
+  if (rows > fit) rows = fit;
+  const int mt = moe_few_share(p, 64 / kHalves, sms) >= 3 ? 4 : moe_few_share(p, 32 / kHalves, sms) >= 3 ? 2 : kHalves;
+  if (rows <= 8) {
+    if (mt == 4) return launch_moe_few<1, 4, kUp, kGated>(W, p, dev, sms, st);
+    if (mt == 2) return launch_moe_few<1, 2, kUp, kGated>(W, p, dev, sms, st);
+    return launch_moe_few<1, kHalves, kUp, kGated>(W, p, dev, sms, st);
+  }
+  if (rows <= 16) {
+    if (mt == 4) return launch_moe_few<2, 4, kUp, kGated>(W, p, dev, sms, st);
+    if (mt == 2) return launch_moe_few<2, 2, kUp, kGated>(W, p, dev, sms, st);
+    return launch_moe_few<2, kHalves, kUp, kGated>(W, p, dev, sms, st);
+  }
+  if (rows <= 32 || kHalves == 2) {
+    if (mt >= 2) return launch_moe_few<4, 2, kUp, kGated>(W, p, dev, sms, st);
+    return launch_moe_few<4, kHalves, kUp, kGated>(W, p, dev, sms, st);
+  }
+  if constexpr (kHalves == 1) return launch_moe_few<8, 1, kUp, kGated>(W, p, dev, sms, st);
+  return FP8Q_ERR_UNSUPPORTED;   // not reached
 }
 
 }  // namespace
@@ -1225,14 +1245,14 @@ fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts,
   p.act = activation;
   p.hidden = static_cast<__half*>(workspace);
   p.y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + moe_layer_y_offset(rows, F));
-  fp8q_status s = gated ? launch_moe_few_nt<true, true>(Wq_up, p, T, dev, sms, st)
-                        : launch_moe_few_nt<true, false>(Wq_up, p, T, dev, sms, st);
+  fp8q_status s = gated ? launch_moe_few_any<true, true>(Wq_up, p, T, dev, sms, st)
+                        : launch_moe_few_any<true, false>(Wq_up, p, T, dev, sms, st);
   if (s != FP8Q_OK) return s;
   p.x = p.hidden;
   p.s_w = s_down;
   p.K = static_cast<int>(F);
   p.n_out = static_cast<int>(N);
-  s = launch_moe_few_nt<false, false>(Wq_down, p, T, dev, sms, st);
+  s = launch_moe_few_any<false, false>(Wq_down, p, T, dev, sms, st);
   if (s != FP8Q_OK) return s;
   const int64_t items = T * (N >> 2);
   const int grid = static_cast<int>(items < 256 * int64_t(sms) ? (items + 255) / 256 : sms);
