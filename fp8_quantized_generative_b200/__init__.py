@@ -26,7 +26,7 @@ the linear's epilogue, the MoE router, and a whole MoE FFN for a few tokens.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 from typing import NamedTuple
 
 import torch
@@ -334,15 +334,30 @@ def _act(name) -> int:
         raise ValueError(f"unknown activation {name!r} (none, relu, gelu, gelu_tanh or silu)") from None
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+# The FFN operators below serve single tokens, where a call's host time counts:
+# arguments pass through one short test each (what it refuses, _need explains),
+# the stream handle is read without building a Stream object, and sizes that
+# the library computes are remembered.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(t: torch.Tensor):
-    """The tensor's device made current for a call (the library launches on the current device)."""
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _arg(t: torch.Tensor, dtype, ndim: int, dev: int, name: str) -> None:
+    """t must be a contiguous CUDA tensor of this dtype and rank on device number dev."""
+    try:
+        if t.dtype is dtype and t.dim() == ndim and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, dtype, name, ndim)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _device(t: torch.Tensor, dtype, name: str, ndim: int) -> int:
+    """The device number of the first argument, which the others must share."""
+    _need(t, dtype, name, ndim)
+    return t.get_device()
 
 
 def linear_epilogue(Xq: torch.Tensor, s_x: torch.Tensor, Wq: torch.Tensor, s_w: torch.Tensor,
@@ -355,34 +370,37 @@ def linear_epilogue(Xq: torch.Tensor, s_x: torch.Tensor, Wq: torch.Tensor, s_w: 
     residual fp16 [M,N], which may be `out` itself."""
     act = _act(activation)
     fmt = _fmt(x_fmt)
-    _need(Xq, torch.uint8, "Xq", 2)
-    _need(Wq, torch.uint8, "Wq", 2)
-    _need(s_x, torch.float32, "s_x", 1)
-    _need(s_w, torch.float32, "s_w", 1)
+    dev = _device(Xq, torch.uint8, "Xq", 2)
+    _arg(Wq, torch.uint8, 2, dev, "Wq")
+    _arg(s_x, torch.float32, 1, dev, "s_x")
+    _arg(s_w, torch.float32, 1, dev, "s_w")
     M, K = Xq.shape
-    N = Wq.shape[0]
-    if Wq.shape[1] != K or s_x.shape[0] != M or s_w.shape[0] != N:
+    N, K2 = Wq.shape
+    if K2 != K or s_x.shape[0] != M or s_w.shape[0] != N:
         raise ValueError("shape mismatch")
+    b = r = 0
     if bias is not None:
-        _need(bias, torch.float16, "bias", 1)
+        _arg(bias, torch.float16, 1, dev, "bias")
         if bias.shape[0] != N:
             raise ValueError("bias must be [N]")
+        b = bias.data_ptr()
     if residual is not None:
-        _need(residual, torch.float16, "residual", 2)
+        _arg(residual, torch.float16, 2, dev, "residual")
         if residual.shape != (M, N):
             raise ValueError("residual must be [M,N]")
+        r = residual.data_ptr()
     if out is not None:
-        _need(out, torch.float16, "out", 2)
+        _arg(out, torch.float16, 2, dev, "out")
         if out.shape != (M, N):
             raise ValueError("out must be [M,N]")
-    _same_device(Xq, s_x=s_x, Wq=Wq, s_w=s_w, bias=bias, residual=residual, out=out)
-    with _on(Xq):
-        Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=Xq.device)
-        check(_lib.fp8q_linear_epilogue(Xq.data_ptr(), fmt, s_x.data_ptr(), Wq.data_ptr(), s_w.data_ptr(), M, N, K,
-                                        bias.data_ptr() if bias is not None else 0, act,
-                                        residual.data_ptr() if residual is not None else 0, Y.data_ptr(), _stream(Xq)),
-              "fp8q_linear_epilogue")
-    return Y
+    if dev != torch.cuda.current_device():   # the library launches on the current device
+        with torch.cuda.device(dev):
+            return linear_epilogue(Xq, s_x, Wq, s_w, bias, activation, residual, out, x_fmt)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.float16, device=Xq.device)
+    check(lib().fp8q_linear_epilogue(Xq.data_ptr(), fmt, s_x.data_ptr(), Wq.data_ptr(), s_w.data_ptr(), M, N, K, b, act,
+                                     r, out.data_ptr(), _raw_stream(dev)), "fp8q_linear_epilogue")
+    return out
 
 
 class MoeRoute(NamedTuple):
@@ -395,6 +413,11 @@ class MoeRoute(NamedTuple):
     token_rows: torch.Tensor   # int32 [T, topk]: the grouped row of each (token, choice)
 
 
+@functools.lru_cache(maxsize=1024)
+def _route_workspace_words(T: int, E: int) -> int:
+    return int(_lib.fp8q_moe_route_workspace_words(T, E))
+
+
 def moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True) -> MoeRoute:
     """MoE router on the device: the topk experts of each token from fp16 gate
     logits [T,E] (ties to the lower expert), their softmax weights (over the
@@ -402,34 +425,39 @@ def moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True) -> MoeR
     rows in the form that quantize_rows_dispatch (token_rows), the grouped
     linears (offsets), the combine (row_token, row_weight) and moe_layer
     (experts, weights) read."""
-    _need(logits, torch.float16, "logits", 2)
+    dev = _device(logits, torch.float16, "logits", 2)
     T, E = logits.shape
     if not 1 <= topk <= min(8, E):
         raise ValueError("topk must be in [1, min(8, E)]")
-    dev = logits.device
+    if dev != torch.cuda.current_device():   # the library launches on the current device
+        with torch.cuda.device(dev):
+            return moe_route(logits, topk, renormalize)
     # one allocation for all outputs (each 16-byte aligned) and the workspace
     rows = T * topk
-    pad = -(-rows // 4) * 4
-    offs = -(-(E + 1) // 4) * 4
-    with _on(logits):
-        words = int(_lib.fp8q_moe_route_workspace_words(T, E))
-        buf = torch.empty((5 * pad + offs + words,), dtype=torch.int32, device=dev)
-        experts, row_token, token_rows = buf[:rows], buf[pad:pad + rows], buf[2 * pad:2 * pad + rows]
-        weights = buf[3 * pad:3 * pad + rows].view(torch.float32)
-        row_weight = buf[4 * pad:4 * pad + rows].view(torch.float32)
-        offsets = buf[5 * pad:5 * pad + E + 1]
-        base = buf.data_ptr()
-        check(_lib.fp8q_moe_route(logits.data_ptr(), T, E, topk, int(bool(renormalize)), base, base + 12 * pad,
-                                  base + 20 * pad, base + 4 * pad, base + 16 * pad, base + 8 * pad,
-                                  base + 4 * (5 * pad + offs) if words else 0, _stream(logits)), "fp8q_moe_route")
-    return MoeRoute(experts.view(T, topk), weights.view(T, topk), offsets, row_token, row_weight,
-                    token_rows.view(T, topk))
+    pad = (rows + 3) & ~3
+    offs = (E + 4) & ~3
+    words = _route_workspace_words(T, E)
+    buf = torch.empty(5 * pad + offs + words, dtype=torch.int32, device=logits.device)
+    base = buf.data_ptr()
+    check(lib().fp8q_moe_route(logits.data_ptr(), T, E, topk, 1 if renormalize else 0, base, base + 12 * pad,
+                               base + 20 * pad, base + 4 * pad, base + 16 * pad, base + 8 * pad,
+                               base + 4 * (5 * pad + offs) if words else 0, _raw_stream(dev)), "fp8q_moe_route")
+    f32 = buf.view(torch.float32)
+    square, line = ((T, topk), (topk, 1)), ((rows,), (1,))
+    return MoeRoute(buf.as_strided(*square, 0), f32.as_strided(*square, 3 * pad),
+                    buf.as_strided((E + 1,), (1,), 5 * pad), buf.as_strided(*line, pad),
+                    f32.as_strided(*line, 4 * pad), buf.as_strided(*square, 2 * pad))
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_workspace_bytes(T: int, topk: int, F: int, N: int) -> int:
+    return int(_lib.fp8q_moe_layer_workspace_bytes(T, topk, F, N))
 
 
 def moe_layer_workspace(T: int, topk: int, F: int, N: int, device) -> torch.Tensor:
     """Workspace of moe_layer for up to T tokens (uint8); reusable across calls
     that do not overlap on the GPU."""
-    return torch.empty((int(_lib.fp8q_moe_layer_workspace_bytes(T, topk, F, N)),), dtype=torch.uint8, device=device)
+    return torch.empty(_layer_workspace_bytes(T, topk, F, N), dtype=torch.uint8, device=device)
 
 
 def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_up: torch.Tensor, s_up: torch.Tensor,
@@ -444,13 +472,13 @@ def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_
     fp16 [T,N] is added (it may be `out` itself).  Larger batches: moe_route and
     the grouped linears."""
     act = _act(activation)
-    _need(X, torch.float16, "X", 2)
-    _need(experts, torch.int32, "experts", 2)
-    _need(weights, torch.float32, "weights", 2)
-    _need(Wq_up, torch.uint8, "Wq_up", 3)
-    _need(s_up, torch.float32, "s_up", 2)
-    _need(Wq_down, torch.uint8, "Wq_down", 3)
-    _need(s_down, torch.float32, "s_down", 2)
+    dev = _device(X, torch.float16, "X", 2)
+    _arg(experts, torch.int32, 2, dev, "experts")
+    _arg(weights, torch.float32, 2, dev, "weights")
+    _arg(Wq_up, torch.uint8, 3, dev, "Wq_up")
+    _arg(s_up, torch.float32, 2, dev, "s_up")
+    _arg(Wq_down, torch.uint8, 3, dev, "Wq_down")
+    _arg(s_down, torch.float32, 2, dev, "s_down")
     T, K = X.shape
     topk = experts.shape[1]
     E, N, F = Wq_down.shape
@@ -458,29 +486,33 @@ def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_
     if (experts.shape[0] != T or weights.shape != experts.shape or Wq_up.shape != (E, up_rows, K)
             or s_up.shape != (E, up_rows) or s_down.shape != (E, N)):
         raise ValueError("shape mismatch")
+    r = 0
     if residual is not None:
-        _need(residual, torch.float16, "residual", 2)
+        _arg(residual, torch.float16, 2, dev, "residual")
         if residual.shape != (T, N):
             raise ValueError("residual must be [T,N]")
+        r = residual.data_ptr()
     if out is not None:
-        _need(out, torch.float16, "out", 2)
+        _arg(out, torch.float16, 2, dev, "out")
         if out.shape != (T, N):
             raise ValueError("out must be [T,N]")
-    _same_device(X, experts=experts, weights=weights, Wq_up=Wq_up, s_up=s_up, Wq_down=Wq_down, s_down=s_down,
-                 residual=residual, workspace=workspace, out=out)
-    need = int(_lib.fp8q_moe_layer_workspace_bytes(T, topk, F, N))
+    need = _layer_workspace_bytes(T, topk, F, N)
     if workspace is not None:
-        _need(workspace, torch.uint8, "workspace", 1)
-        if workspace.numel() < need:
+        _arg(workspace, torch.uint8, 1, dev, "workspace")
+        if workspace.shape[0] < need:
             raise ValueError("workspace does not fit this call")
-    with _on(X):
-        Y = out if out is not None else torch.empty((T, N), dtype=torch.float16, device=X.device)
-        ws = workspace if workspace is not None else torch.empty((need,), dtype=torch.uint8, device=X.device)
-        check(_lib.fp8q_moe_layer(X.data_ptr(), T, experts.data_ptr(), weights.data_ptr(), topk, E, Wq_up.data_ptr(),
-                                  s_up.data_ptr(), Wq_down.data_ptr(), s_down.data_ptr(), K, F, N, act,
-                                  int(bool(gated)), residual.data_ptr() if residual is not None else 0, Y.data_ptr(),
-                                  ws.data_ptr(), _stream(X)), "fp8q_moe_layer")
-    return Y
+    if dev != torch.cuda.current_device():   # the library launches on the current device
+        with torch.cuda.device(dev):
+            return moe_layer(X, experts, weights, Wq_up, s_up, Wq_down, s_down, activation, gated, residual, workspace,
+                             out)
+    if out is None:
+        out = torch.empty(T, N, dtype=torch.float16, device=X.device)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+    check(lib().fp8q_moe_layer(X.data_ptr(), T, experts.data_ptr(), weights.data_ptr(), topk, E, Wq_up.data_ptr(),
+                               s_up.data_ptr(), Wq_down.data_ptr(), s_down.data_ptr(), K, F, N, act, 1 if gated else 0,
+                               r, out.data_ptr(), workspace.data_ptr(), _raw_stream(dev)), "fp8q_moe_layer")
+    return out
 
 
 def e4m3_encode_f32(x: torch.Tensor) -> torch.Tensor:

@@ -131,7 +131,6 @@ template <int kMaxChunks>
 struct EpiScales {
   float sx;
   float sw[kMaxChunks];
-  float sb[kMaxChunks];   // kEpi: the bias of the same columns
   float rw;    // combine: weight of this lane's row
   int ctok;    // combine: output (token) row of this lane's row, -1: none
 };
@@ -158,9 +157,7 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
 #pragma unroll
   for (int j = 0; j < kMaxChunks; ++j) {
     const int cl = w.col0 + j * 32 + lane;
-    e.sw[j] = (j < w.nch && t.n0 + cl < p.N) ? __ldg(p.s_w + t.sw0 + cl) : 0.0f;
-    // no bias: adding -0 leaves every value, -0 included, as it is
-    if (kEpi) e.sb[j] = (p.bias != nullptr && j < w.nch && t.n0 + cl < p.N) ? __half2float(__ldg(p.bias + t.n0 + cl)) : -0.0f;
+    if (!kEpi) e.sw[j] = (j < w.nch && t.n0 + cl < p.N) ? __ldg(p.s_w + t.sw0 + cl) : 0.0f;
   }
   return e;
 }
@@ -168,47 +165,86 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
 // The epilogue of the dense linear with bias, activation and residual, on the
 // 32 columns of one chunk that a lane holds: z = (acc * s_x) * s_w as the
 // plain linear computes it, then z + bias, the activation, + residual, each
-// fp32 and rounded to nearest; the caller rounds once to fp16.  `res` holds
-// the lane's 32 residual values (used when p.residual is set).
-template <int kMaxChunks>
-__device__ __forceinline__ void epilogue_values(float (&z)[32], const GemmParams& p, const EpiScales<kMaxChunks>& pre,
-                                                int j, const uint4 (&res)[4]) {
+// fp32 and rounded to nearest; one rounding to fp16.
+//
+// What a chunk needs besides the accumulators.  s_w and the bias are read by all
+// lanes at the same address (one wavefront for four columns, where handing them
+// round by shuffles takes two instructions a column); the residual by a lane for its
+// own row.  Columns at or past N are not read (N % 8 == 0: groups of 8 are all in or
+// all out).
+struct EpiChunk {
+  float4 w[8];
+  uint4 b[4];
+  uint4 r[4];
+};
+
+__device__ __forceinline__ void epilogue_residual(EpiChunk& c, const GemmParams& p, int row, bool row_ok, int n) {
+  if (p.residual == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float w = __shfl_sync(0xffffffffu, pre.sw[j], i);
-    const float b = __shfl_sync(0xffffffffu, pre.sb[j], i);
-    z[i] = __fadd_rn(__fmul_rn(__fmul_rn(z[i], pre.sx), w), b);
+  for (int i = 0; i < 4; ++i) {
+    c.r[i] = make_uint4(0, 0, 0, 0);
+    if (row_ok && n + 8 * i < p.N) c.r[i] = ld_global_v4(p.residual + static_cast<int64_t>(row) * p.N + n + 8 * i);
   }
-  switch (p.act) {   // uniform: one branch per chunk
-    case kActRelu:
+}
+
+__device__ __forceinline__ void epilogue_columns(EpiChunk& c, const GemmParams& p, int n) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActRelu);
-      break;
-    case kActGelu:
+  for (int i = 0; i < 4; ++i) {
+    const bool in = n + 8 * i < p.N;
+    c.w[2 * i] = c.w[2 * i + 1] = make_float4(0, 0, 0, 0);
+    c.b[i] = make_uint4(0, 0, 0, 0);
+    if (in) {
+      c.w[2 * i] = __ldg(reinterpret_cast<const float4*>(p.s_w + n + 8 * i));
+      c.w[2 * i + 1] = __ldg(reinterpret_cast<const float4*>(p.s_w + n + 8 * i + 4));
+      if (p.bias != nullptr) c.b[i] = __ldg(reinterpret_cast<const uint4*>(p.bias + n + 8 * i));
+    }
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate_pairs(F32x2 (&z)[16]) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActGelu);
-      break;
-    case kActGeluTanh:
+  for (int i = 0; i < 16; ++i) z[i] = activate2<ACT>(z[i]);
+}
+
+// acc: 32 accumulators of the lane's row -> 16 packed fp16 pairs.
+__device__ __forceinline__ void epilogue_values(const uint32_t (&acc)[32], float sx, const EpiChunk& c,
+                                                const GemmParams& p, uint32_t (&packed)[16]) {
+  F32x2 z[16];
+  const F32x2 sx2 = both(sx);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActGeluTanh);
-      break;
-    case kActSilu:
+  for (int i = 0; i < 16; ++i) {
+    const float4 w = c.w[i >> 1];
+    z[i] = mul2(mul2(pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1])), sx2),
+                i & 1 ? pack2(w.z, w.w) : pack2(w.x, w.y));
+  }
+  if (p.bias != nullptr) {   // uniform, as the branches below
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = activate(z[i], kActSilu);
-      break;
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = __half22float2(reinterpret_cast<const __half2*>(&c.b[i >> 2])[i & 3]);
+      z[i] = add2(z[i], pack2(f.x, f.y));
+    }
+  }
+  switch (p.act) {
+    case kActRelu: activate_pairs<kActRelu>(z); break;
+    case kActGelu: activate_pairs<kActGelu>(z); break;
+    case kActGeluTanh: activate_pairs<kActGeluTanh>(z); break;
+    case kActSilu: activate_pairs<kActSilu>(z); break;
     default: break;
   }
   if (p.residual != nullptr) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const __half2* h = reinterpret_cast<const __half2*>(&res[c]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        z[c * 8 + 2 * i] = __fadd_rn(z[c * 8 + 2 * i], f.x);
-        z[c * 8 + 2 * i + 1] = __fadd_rn(z[c * 8 + 2 * i + 1], f.y);
-      }
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = __half22float2(reinterpret_cast<const __half2*>(&c.r[i >> 2])[i & 3]);
+      z[i] = add2(z[i], pack2(f.x, f.y));
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    unpack2(z[i], a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    packed[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
@@ -259,23 +295,10 @@ __device__ __forceinline__ void epilogue_slab(const EpiTile& t, const GemmParams
     if (j + 1 < nch) tmem_ld_32x32b_x32(taddr0 + static_cast<uint32_t>((j + 1) * 32), v[(j + 1) & 1]);
     uint32_t packed[16];
     if constexpr (kEpi) {
-      uint4 res[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int gcol = t.n0 + cl + c * 8;
-        res[c] = make_uint4(0, 0, 0, 0);
-        if (p.residual != nullptr && lane < valid && gcol < p.N)
-          res[c] = ld_global_v4(p.residual + static_cast<int64_t>(qrow0 + lane) * p.N + gcol);
-      }
-      float z[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(cur[i]);
-      epilogue_values<kMaxChunks>(z, p, pre, j, res);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const __half2 hv = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
-        packed[i] = *reinterpret_cast<const uint32_t*>(&hv);
-      }
+      EpiChunk c;
+      epilogue_residual(c, p, qrow0 + lane, lane < valid, t.n0 + cl);
+      epilogue_columns(c, p, t.n0 + cl);
+      epilogue_values(v[j & 1], pre.sx, c, p, packed);
     } else
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

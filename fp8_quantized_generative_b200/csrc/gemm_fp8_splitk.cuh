@@ -83,10 +83,8 @@ struct SplitKLayout {
 // receive buffer) summed in rank order 0..S-1, scaled and stored as fp16.
 // Each of the 128 epilogue threads takes blocks of 4 token rows x 8 weight
 // rows: eight 16-byte shared loads per slice, one 16-byte global store per
-// token row (the 8 outputs are consecutive columns of Y).  kEpi: bias,
-// activation and residual after the scales (the residual is read by the
-// thread that then writes the same 8 outputs, so it may be Y itself).
-template <int S, typename L, bool kEpi>
+// token row (the 8 outputs are consecutive columns of Y).
+template <int S, typename L>
 __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const float* send, const float* recv,
                                                     const float* sc_w, const float* sc_x, int n0, int rank, int et) {
   constexpr int SL = kBM / S;
@@ -102,14 +100,6 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
     const int nl0 = (idx / m4n) * 8;
     const int n = n0 + rank * SL + nl0;
     if (n >= p.N) continue;                        // N % 8 == 0: a block is all in or all out
-    uint4 res[4], bias = make_uint4(0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u);   // -0: adds nothing
-    if constexpr (kEpi) {
-      if (p.bias != nullptr) bias = __ldg(reinterpret_cast<const uint4*>(p.bias + n));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p.residual != nullptr && m + i < p.rows)
-          res[i] = ld_global_v4(p.residual + static_cast<int64_t>(m + i) * p.N + n);
-    }
     float acc[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
@@ -134,21 +124,6 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
       if (m + i >= p.rows) break;
       const float sx = sc_x[m + i];
       uint32_t w[4];
-      if constexpr (kEpi) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float2 b = __half22float2(reinterpret_cast<const __half2*>(&bias)[j / 2]);
-          float y0 = activate(__fadd_rn(__fmul_rn(__fmul_rn(acc[j][i], sx), sw[j]), b.x), p.act);
-          float y1 = activate(__fadd_rn(__fmul_rn(__fmul_rn(acc[j + 1][i], sx), sw[j + 1]), b.y), p.act);
-          if (p.residual != nullptr) {
-            const float2 r = __half22float2(reinterpret_cast<const __half2*>(&res[i])[j / 2]);
-            y0 = __fadd_rn(y0, r.x);
-            y1 = __fadd_rn(y1, r.y);
-          }
-          const __half2 h = __floats2half2_rn(y0, y1);
-          w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      } else
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const __half2 h = __floats2half2_rn(__fmul_rn(__fmul_rn(acc[j][i], sx), sw[j]),
@@ -157,6 +132,88 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
       }
       *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(m + i) * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+}
+
+// The same with bias, activation and residual after the scales.  An activation
+// costs more than the sum, so the work is cut finer: an item is one token row x
+// WB weight rows (8, one 16-byte store; 2 where that would leave threads
+// idle), token rows fastest across threads (consecutive words of a partial
+// row).  Bias and residual of a thread's first item are loaded before the
+// mainloop ends (SplitKEpi), the rest when their item comes.  The residual is read by
+// the thread that writes the same outputs, so it may be Y itself.
+template <int WB>
+struct SplitKEpi {
+  alignas(16) __half b[WB];
+  alignas(16) __half r[WB];
+};
+
+template <int WB>
+__device__ __forceinline__ void splitk_epi_load(SplitKEpi<WB>& e, const GemmParams& p, int m, int n) {
+  static_assert(WB == 8 || WB == 2, "WB");
+  const int64_t at = static_cast<int64_t>(m) * p.N + n;
+  if constexpr (WB == 8) {
+    if (p.bias != nullptr) *reinterpret_cast<uint4*>(e.b) = __ldg(reinterpret_cast<const uint4*>(p.bias + n));
+    if (p.residual != nullptr) *reinterpret_cast<uint4*>(e.r) = ld_global_v4(p.residual + at);
+  } else {
+    if (p.bias != nullptr) *reinterpret_cast<uint32_t*>(e.b) = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
+    if (p.residual != nullptr) *reinterpret_cast<uint32_t*>(e.r) = ld_global_u32(p.residual + at);
+  }
+}
+
+// Item idx of an owner's share: token row and first of its weight rows.
+template <int WB>
+__device__ __forceinline__ void splitk_epi_item(const GemmParams& p, int idx, int& m, int& nl) {
+  nl = idx / p.rows * WB;
+  m = idx - nl / WB * p.rows;
+}
+
+template <int S, typename L, int WB>
+__device__ __forceinline__ void splitk_epi_store(const GemmParams& p, const float* send, const float* recv,
+                                                 const float* sc_w, const float* sc_x, int n0, int rank, int et,
+                                                 SplitKEpi<WB> e) {
+  constexpr int SL = kBM / S;
+  const int items = p.rows * (SL / WB);
+  for (int idx = et; idx < items; idx += 128) {
+    int m, nl;
+    splitk_epi_item<WB>(p, idx, m, nl);
+    const int n = n0 + rank * SL + nl;
+    if (n >= p.N) continue;                        // N % 8 == 0: an item is all in or all out
+    if (idx != et) splitk_epi_load<WB>(e, p, m, n);
+    float z[WB];
+#pragma unroll
+    for (int j = 0; j < WB; ++j) z[j] = 0.0f;
+#pragma unroll
+    for (int s2 = 0; s2 < S; ++s2) {               // rank order, as the plain linear
+      const float* base = (s2 == rank ? send + (rank * SL + nl) * L::kPitch : recv + (s2 * SL + nl) * L::kPitch) + m;
+#pragma unroll
+      for (int j = 0; j < WB; ++j) z[j] = __fadd_rn(z[j], base[j * L::kPitch]);
+    }
+    const float sx = sc_x[m];
+    __half2 h[WB / 2];
+#pragma unroll
+    for (int j = 0; j < WB; ++j) {
+      z[j] = __fmul_rn(__fmul_rn(z[j], sx), sc_w[nl + j]);
+      if (p.bias != nullptr) z[j] = __fadd_rn(z[j], __half2float(e.b[j]));
+      z[j] = activate(z[j], p.act);
+      if (p.residual != nullptr) z[j] = __fadd_rn(z[j], __half2float(e.r[j]));
+      if (j & 1) h[j / 2] = __floats2half2_rn(z[j - 1], z[j]);
+    }
+    __half* y = p.Y + static_cast<int64_t>(m) * p.N + n;
+    if constexpr (WB == 8) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(h);
+    else *reinterpret_cast<__half2*>(y) = h[0];
+  }
+}
+
+template <typename L, int WB>
+__device__ __forceinline__ void splitk_epi_store_any(const GemmParams& p, const float* send, const float* recv,
+                                                     const float* sc_w, const float* sc_x, int n0, int rank, int et,
+                                                     int S, const SplitKEpi<WB>& e) {
+  switch (S) {
+    case 1: splitk_epi_store<1, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    case 2: splitk_epi_store<2, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    case 4: splitk_epi_store<4, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    default: splitk_epi_store<8, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
   }
 }
 
@@ -354,6 +411,19 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       if (et < SL) sc_w[et] = n < p.N ? __ldg(p.s_w + n) : 0.0f;
       if (!kFused && et < p.rows) sc_x[et] = __ldg(p.s_x + et);
     }
+    const bool wide = p.rows * SL >= 8 * 128;   // kEpi: items of eight weight rows keep every thread busy
+    SplitKEpi<8> e8;
+    SplitKEpi<2> e2;
+    if constexpr (kEpi) {
+      int m, nl;
+      if (wide) splitk_epi_item<8>(p, et, m, nl);
+      else splitk_epi_item<2>(p, et, m, nl);
+      const int n = n0 + rank * SL + nl;
+      if (nl < SL && n < p.N) {
+        if (wide) splitk_epi_load<8>(e8, p, m, n);
+        else splitk_epi_load<2>(e2, p, m, n);
+      }
+    }
     if (kFused) {
       // Per-token dynamic quantization of the rows this CTA multiplies,
       // shared by the S CTAs of the cluster, each of which reads only its
@@ -515,12 +585,15 @@ __global__ void __launch_bounds__(kSkThreads, 1)
     if (!mbar_wait(recv_bar, 0, abort_flag)) {
       raise_error(0x10u);
       *abort_flag = 1;
+    } else if constexpr (kEpi) {
+      if (wide) splitk_epi_store_any<L, 8>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e8);
+      else splitk_epi_store_any<L, 2>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e2);
     } else {
       switch (S) {
-        case 1: splitk_reduce_store<1, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
-        case 2: splitk_reduce_store<2, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
-        case 4: splitk_reduce_store<4, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
-        default: splitk_reduce_store<8, L, kEpi>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        case 1: splitk_reduce_store<1, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        case 2: splitk_reduce_store<2, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        case 4: splitk_reduce_store<4, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
+        default: splitk_reduce_store<8, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
       }
     }
   }

@@ -431,6 +431,12 @@ __device__ __forceinline__ uint4 ld_global_v4(const void* ptr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t ld_global_u32(const void* ptr) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
+  return v;
+}
+
 // 2-D tiled bulk tensor store shared -> global (elements outside the tensor
 // are not written).  x is the innermost coordinate in elements.
 __device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t x, int32_t y) {
