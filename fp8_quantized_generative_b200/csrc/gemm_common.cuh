@@ -167,37 +167,53 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
 // plain linear computes it, then z + bias, the activation, + residual, each
 // fp32 and rounded to nearest; one rounding to fp16.
 //
-// What a chunk needs besides the accumulators.  s_w and the bias are read by all
-// lanes at the same address (one wavefront for four columns, where handing them
-// round by shuffles takes two instructions a column); the residual by a lane for its
-// own row.  Columns at or past N are not read (N % 8 == 0: groups of 8 are all in or
-// all out).
-struct EpiChunk {
-  float4 w[8];
-  uint4 b[4];
-  uint4 r[4];
+// What it needs besides the accumulators:
+//   * s_w and the bias of the tile's columns, which the four warps of a column half
+//     stage in shared memory while the tile's MMAs run, and all lanes read at the
+//     same address (one 16-byte read for four scales or eight biases, where handing
+//     them round by shuffles takes an instruction a column);
+//   * the residual of the chunk's 32 x 32 values, loaded a chunk ahead four lanes to
+//     a row (whole sectors) and turned into rows through the staging tile, which is
+//     free then.
+constexpr int kEpiColBytes = 256 * (4 + 2);   // s_w fp32, bias fp16 of up to 256 columns (512-wide tiles have no kEpi form)
+struct EpiCols {
+  float* w;     // [256]
+  __half* b;    // [256]
 };
-
-__device__ __forceinline__ void epilogue_residual(EpiChunk& c, const GemmParams& p, int row, bool row_ok, int n) {
-  if (p.residual == nullptr) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c.r[i] = make_uint4(0, 0, 0, 0);
-    if (row_ok && n + 8 * i < p.N) c.r[i] = ld_global_v4(p.residual + static_cast<int64_t>(row) * p.N + n + 8 * i);
-  }
+__device__ __forceinline__ EpiCols epi_cols(void* after_bars) {
+  EpiCols c;
+  c.w = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(after_bars) + 15) & ~uintptr_t(15));
+  c.b = reinterpret_cast<__half*>(c.w + 256);
+  return c;
 }
 
-__device__ __forceinline__ void epilogue_columns(EpiChunk& c, const GemmParams& p, int n) {
+// Stage the columns of one half (h = 0 or 1) of a bn-wide tile: called by the
+// half's four warps (named barrier 2 + h, 128 threads) before they wait for the
+// accumulator; the first barrier ends their reads of the tile before.
+__device__ __forceinline__ void epilogue_stage_columns(const EpiCols& c, const GemmParams& p, int n0, int bn, int warp,
+                                                       int lane) {
+  const int h = (warp - kEpiWarp0) >> 2;
+  const int i = (warp & 3) * 32 + lane;
+  const int col = h * (bn / 2) + i;
+  const bool mine = i < bn / 2, in = mine && n0 + col < p.N;
+  const float w = in ? __ldg(p.s_w + n0 + col) : 0.0f;
+  const __half b = in && p.bias != nullptr ? __ldg(p.bias + n0 + col) : __float2half_rn(0.0f);
+  named_barrier(2 + h, 128);
+  if (mine) {
+    c.w[col] = w;
+    c.b[col] = b;
+  }
+  named_barrier(2 + h, 128);
+}
+
+// Residual of a chunk (32 rows from row0, 32 columns from n), four lanes to a row:
+// r[it] holds columns 8 (lane & 3) .. + 7 of row 8 it + lane / 4.
+__device__ __forceinline__ void epilogue_residual(uint4 (&r)[4], const GemmParams& p, int row0, int rows, int n, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool in = n + 8 * i < p.N;
-    c.w[2 * i] = c.w[2 * i + 1] = make_float4(0, 0, 0, 0);
-    c.b[i] = make_uint4(0, 0, 0, 0);
-    if (in) {
-      c.w[2 * i] = __ldg(reinterpret_cast<const float4*>(p.s_w + n + 8 * i));
-      c.w[2 * i + 1] = __ldg(reinterpret_cast<const float4*>(p.s_w + n + 8 * i + 4));
-      if (p.bias != nullptr) c.b[i] = __ldg(reinterpret_cast<const uint4*>(p.bias + n + 8 * i));
-    }
+  for (int it = 0; it < 4; ++it) {
+    const int row = it * 8 + (lane >> 2), col = n + (lane & 3) * 8;
+    r[it] = make_uint4(0, 0, 0, 0);
+    if (row < rows && col < p.N) r[it] = ld_global_v4(p.residual + static_cast<int64_t>(row0 + row) * p.N + col);
   }
 }
 
@@ -207,44 +223,104 @@ __device__ __forceinline__ void activate_pairs(F32x2 (&z)[16]) {
   for (int i = 0; i < 16; ++i) z[i] = activate2<ACT>(z[i]);
 }
 
-// acc: 32 accumulators of the lane's row -> 16 packed fp16 pairs.
-__device__ __forceinline__ void epilogue_values(const uint32_t (&acc)[32], float sx, const EpiChunk& c,
-                                                const GemmParams& p, uint32_t (&packed)[16]) {
-  F32x2 z[16];
-  const F32x2 sx2 = both(sx);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float4 w = c.w[i >> 1];
-    z[i] = mul2(mul2(pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1])), sx2),
-                i & 1 ? pack2(w.z, w.w) : pack2(w.x, w.y));
-  }
-  if (p.bias != nullptr) {   // uniform, as the branches below
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 f = __half22float2(reinterpret_cast<const __half2*>(&c.b[i >> 2])[i & 3]);
-      z[i] = add2(z[i], pack2(f.x, f.y));
-    }
-  }
-  switch (p.act) {
+__device__ __forceinline__ void activate_pairs_any(F32x2 (&z)[16], int act) {
+  switch (act) {   // uniform
     case kActRelu: activate_pairs<kActRelu>(z); break;
     case kActGelu: activate_pairs<kActGelu>(z); break;
     case kActGeluTanh: activate_pairs<kActGeluTanh>(z); break;
     case kActSilu: activate_pairs<kActSilu>(z); break;
     default: break;
   }
-  if (p.residual != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 f = __half22float2(reinterpret_cast<const __half2*>(&c.r[i >> 2])[i & 3]);
-      z[i] = add2(z[i], pack2(f.x, f.y));
+}
+
+// epilogue_slab (below) with bias, activation and residual.  `cols`: the tile's
+// staged columns; `res`: the residual of the warp's first chunk (a chunk's
+// residual is read before the same warp stores the chunk, so it may be Y itself).
+// The chunk loop stays rolled and the activations are the only code that is there
+// once for each kind: unrolled like the plain slab it ran out of the instruction
+// cache (4096 x 8192 x 1024 with GELU: 63 us).  Once a chunk is scaled its
+// accumulator registers take the TMEM load of the next, in flight during the
+// activation.
+template <int kBufs>
+__device__ __forceinline__ void epilogue_slab_epi(const EpiTile& t, const GemmParams& p, const CUtensorMap* tmY,
+                                                  uint32_t tmem_acc, const EpiWarpView& w, int warp, int lane,
+                                                  uint8_t* stage, float sx, const EpiCols& cols, uint4 (&res)[4]) {
+  const int q = warp & 3;
+  const int valid = t.row_end - w.qrow0;   // rows of this warp that are stored (<= 0: none)
+  if (valid <= 0) return;
+  const uint32_t taddr0 = tmem_acc + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(w.tcol0);
+  const F32x2 sx2 = both(sx);
+  uint32_t v[32];
+  tmem_ld_32x32b_x32(taddr0, v);
+  if (kBufs == 2 && lane == 0) bulk_wait_read_all();
+#pragma unroll 1
+  for (int j = 0; j < w.nch; ++j) {
+    const int cl = w.col0 + j * 32;   // first column of the chunk within the tile
+    uint8_t* buf = stage + (kBufs == 2 ? (j & 1) * kEpiWarps * kStageTileBytes : 0);
+    const uint32_t sbase = smem_u32(buf);
+    // the staging tile must have been read by its last bulk store
+    if (lane == 0) {
+      if (kBufs == 2) bulk_wait_read_1();
+      else bulk_wait_read_all();
     }
-  }
+    __syncwarp();
+    if (p.residual != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float a, b;
-    unpack2(z[i], a, b);
-    const __half2 h = __floats2half2_rn(a, b);
-    packed[i] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int it = 0; it < 4; ++it)
+        st_shared_v4(sbase + stage_off(it * 8 + (lane >> 2), lane & 3), res[it].x, res[it].y, res[it].z, res[it].w);
+      if (j + 1 < w.nch) epilogue_residual(res, p, w.qrow0, valid, t.n0 + cl + 32, lane);
+    }
+    F32x2 z[16];
+    tmem_ld_wait_regs(v);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float4 s = *reinterpret_cast<const float4*>(cols.w + cl + 2 * i);
+      z[i] = mul2(mul2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sx2), pack2(s.x, s.y));
+      z[i + 1] = mul2(mul2(pack2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), sx2), pack2(s.z, s.w));
+    }
+    if (p.bias != nullptr) {   // uniform, as the branches below
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const uint4 b = *reinterpret_cast<const uint4*>(cols.b + cl + 2 * i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(reinterpret_cast<const __half2*>(&b)[k]);
+          z[i + k] = add2(z[i + k], pack2(f.x, f.y));
+        }
+      }
+    }
+    if (j + 1 < w.nch) tmem_ld_32x32b_x32(taddr0 + static_cast<uint32_t>((j + 1) * 32), v);
+    activate_pairs_any(z, p.act);
+    if (p.residual != nullptr) {
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 r = ld_shared_v4(sbase + stage_off(lane, c));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(reinterpret_cast<const __half2*>(&r)[k]);
+          z[4 * c + k] = add2(z[4 * c + k], pack2(f.x, f.y));
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a, b;
+        unpack2(z[4 * c + k], a, b);
+        const __half2 hv = __floats2half2_rn(a, b);
+        h[k] = *reinterpret_cast<const uint32_t*>(&hv);
+      }
+      st_shared_v4(sbase + stage_off(lane, c), h[0], h[1], h[2], h[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tmY, buf, t.n0 + cl, w.qrow0);   // dense: rows past the end lie past the tensor
+      bulk_commit_group();
+    }
   }
 }
 
@@ -261,10 +337,7 @@ __device__ __forceinline__ void epilogue_values(const uint32_t (&acc)[32], float
 // scales per chunk and waited out every load and store measured no faster
 // on the dense shapes and up to 12% slower on the MoE kernels.)
 // w.nch <= kMaxChunks.
-// kEpi: bias, activation and residual (epilogue_values).  A lane reads the
-// residual of its own row, 64 bytes a chunk, before the chunk is stored by
-// the same warp, so the residual may be Y itself.
-template <int kMaxChunks, int kBufs, bool kEpi = false>
+template <int kMaxChunks, int kBufs>
 __device__ __forceinline__ void epilogue_slab(const EpiTile& t, const GemmParams& p, const CUtensorMap* tmY,
                                               uint32_t tmem_acc, const EpiWarpView& w, int warp, int lane,
                                               uint8_t* stage, const EpiScales<kMaxChunks>& pre) {
@@ -294,12 +367,6 @@ __device__ __forceinline__ void epilogue_slab(const EpiTile& t, const GemmParams
     const uint32_t* cur = v[j & 1];
     if (j + 1 < nch) tmem_ld_32x32b_x32(taddr0 + static_cast<uint32_t>((j + 1) * 32), v[(j + 1) & 1]);
     uint32_t packed[16];
-    if constexpr (kEpi) {
-      EpiChunk c;
-      epilogue_residual(c, p, qrow0 + lane, lane < valid, t.n0 + cl);
-      epilogue_columns(c, p, t.n0 + cl);
-      epilogue_values(v[j & 1], pre.sx, c, p, packed);
-    } else
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float w0 = __shfl_sync(0xffffffffu, pre.sw[j], 2 * i);

@@ -350,6 +350,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     uint8_t* stage = sEpi + (warp - kEpiWarp0) * kStageTileBytes;
+    const EpiCols cols = kEpi ? epi_cols(tile_prefix) : EpiCols{};
+    uint4 res[4];   // kEpi: residual of the next chunk
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -362,14 +364,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       et.clip = !kGrouped;   // dense: rows past the end are past the tensor
       const EpiWarpView wv = epi_view(et, warp, BN, false);
       const EpiScales<BN / 64> sc = epilogue_scales<BN / 64, kEpi>(et, p, wv, lane);
+      if constexpr (kEpi) {
+        epilogue_stage_columns(cols, p, c.n0, BN, warp, lane);
+        if (p.residual != nullptr)
+          epilogue_residual(res, p, wv.qrow0, c.row_end - wv.qrow0, c.n0 + wv.col0, lane);
+      }
       if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
         raise_error(0x4u);
         *abort_flag = 1;
+        if constexpr (kEpi) continue;   // the warps of a column half meet at barriers: all walk on
         break;
       }
       tc_fence_after();
-      epilogue_slab<BN / 64, L::kEpiBufs, kEpi>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
-                                          stage, sc);
+      if constexpr (kEpi)
+        epilogue_slab_epi<L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp,
+                                                lane, stage, sc.sx, cols, res);
+      else
+        epilogue_slab<BN / 64, L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
+                                            stage, sc);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[acc]);

@@ -400,6 +400,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             static_cast<int>(gridDim.x) * kEpiWarps, p.rows, lane);
     }
     uint8_t* stage = sEpi + (warp - kEpiWarp0) * kStageTileBytes;
+    const EpiCols cols = kEpi ? epi_cols(tile_prefix) : EpiCols{};
+    uint4 res[4];   // kEpi: residual of the next chunk
     const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
     int acc = 0;
@@ -426,14 +428,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int r = wv.qrow0 + lane;
         sc.sx = r < et.row_end ? ld_relaxed_gpu_f32(p.s_x + r) : 0.0f;
       }
+      if constexpr (kEpi) {
+        epilogue_stage_columns(cols, p, pt.n0, pt.bn, warp, lane);
+        if (p.residual != nullptr)
+          epilogue_residual(res, p, wv.qrow0, pt.row_end - wv.qrow0, pt.n0 + wv.col0, lane);
+      }
       if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
         raise_error(0x4u);
         *abort_flag = 1;
+        if constexpr (kEpi) continue;   // the warps of a column half meet at barriers: all walk on
         break;
       }
       tc_fence_after();
-      epilogue_slab<BN / 64, L::kEpiBufs, kEpi>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
-                                          stage, sc);
+      if constexpr (kEpi)
+        epilogue_slab_epi<L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp,
+                                                lane, stage, sc.sx, cols, res);
+      else
+        epilogue_slab<BN / 64, L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
+                                            stage, sc);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
