@@ -2,22 +2,24 @@
 // in fp32 on values that are rounded to fp16 right after.
 //
 // Accuracy: the target is an error far under half an fp16 step (2^-11
-// relative), at a cost that hides behind the tensor-core mainloop.  Each of the
-// three smooth ones is two special-function operations (ex2.approx and
-// rcp.approx, relative error about 2^-22 each) and a few multiply-adds:
+// relative), at a cost that hides behind the tensor-core mainloop: few special
+// functions (ex2.approx, rcp.approx: relative error about 2^-22 each; 16 a cycle and
+// SM, so each costs as much as eight multiply-adds) and few multiply-adds.
 //   silu       z / (1 + e^-z)
 //   gelu_tanh  0.5 z (1 + tanh u) = z / (1 + e^-2u),  u = sqrt(2/pi) (z + 0.044715 z^3)
-//   gelu       z Phi(z) = max(z, 0) - |z| Phi(-|z|), Phi the normal distribution
-//              function: with u = |z| and t = 1 / (1 + 0.3 u),
-//              Phi(-u) = e^(-u^2/2) t P(t).  P, of degree 5, is a least-squares fit
-//              (reweighted towards the largest relative error) of
-//              erfcx(u / sqrt(2)) / (2 t) over 0 <= u <= 9: relative error 2.1e-6, which
-//              the factored exponential carries to the far negative tail (3.6e-6
-//              relative in fp32 for |z| < 6, past which fp16 has no value left).
+//              Both: one exponential a value and one reciprocal for two, 1/a = b / (ab).
+//              The exponent of 2 is cut at 60, which keeps the product finite; past it
+//              the result is under 2^-43.
+//   gelu       z Phi(z) = max(z, 0) - u Phi(-u) with u = |z|, Phi the normal
+//              distribution function, whose log2 Phi(-u) is smooth: a polynomial of
+//              degree 7, a least-squares fit over 0 <= u <= 6 reweighted towards the
+//              largest error, gives Phi(-u) to a relative 3.3e-6 (6.6e-6 evaluated in
+//              fp32, the far negative tail included) with one exponential.  u is cut at
+//              6: u Phi(-u) is below 6e-9 from there on, under half of fp16's least step.
 // The pair forms do the multiply-adds of two values in one instruction
-// (f32x2, the same roundings): the large GEMM's epilogue has 32768 values a tile and
-// SM, whose special functions take 4100 cycles and whose mainloop 8900 at K = 2048.
-// NaN stays NaN; relu(-0) = -0.
+// (f32x2, the same roundings).  4096 x 8192 x 256, where the epilogue is all the time:
+// GELU 44.6 us with a division and an exponential a value, SILU 40.6.
+// NaN stays NaN.
 #pragma once
 
 #include <cstdint>
@@ -34,6 +36,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The larger value, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
 
@@ -67,17 +76,18 @@ constexpr float kLog2e = 1.44269504088896f;
 // -2 u log2(e) = z (kTanh0 + kTanh1 z^2)
 constexpr float kTanh0 = -1.59576912160573f * kLog2e;    // -2 sqrt(2/pi) log2(e)
 constexpr float kTanh1 = -0.0713548162726009f * kLog2e;  // the same times 0.044715
-constexpr float kGeluC = 0.3f;
-constexpr float kGeluP0 = 0.120327727f, kGeluP1 = 0.111210456f, kGeluP2 = 0.153751159f, kGeluP3 = -0.0340378628f,
-                kGeluP4 = 0.230586332f, kGeluP5 = -0.0818373346f;
+constexpr float kGateCut = 60.0f;
+constexpr float kGeluCut = 6.0f;
+// log2 Phi(-u) = kGelu0 + u (kGelu1 + ..)
+constexpr float kGelu0 = -0.999995294f, kGelu1 = -1.15125105f, kGelu2 = -0.458464391f, kGelu3 = -0.0539600711f,
+                kGelu4 = 0.00850789188f, kGelu5 = -0.000930525087f, kGelu6 = 6.15983236e-05f, kGelu7 = -1.83481289e-06f;
 
-// z times sigmoid, e2 = the exponent of 2 that is e^-x of the sigmoid's argument
+// z / (1 + 2^e2)
 __device__ __forceinline__ F32x2 gate2(F32x2 z, F32x2 e2) {
   float a, b;
   unpack2(e2, a, b);
-  const F32x2 d = add2(pack2(ex2_approx(a), ex2_approx(b)), both(1.0f));
-  unpack2(d, a, b);
-  return mul2(z, pack2(rcp_approx(a), rcp_approx(b)));
+  unpack2(add2(pack2(ex2_approx(fminf(a, kGateCut)), ex2_approx(fminf(b, kGateCut))), both(1.0f)), a, b);
+  return mul2(z, mul2(both(rcp_approx(__fmul_rn(a, b))), pack2(b, a)));
 }
 
 // ACT on two values.
@@ -88,41 +98,40 @@ __device__ __forceinline__ F32x2 activate2(F32x2 z) {
   if (ACT == kActGeluTanh) return gate2(z, mul2(z, fma2(mul2(z, z), both(kTanh1), both(kTanh0))));
   float z0, z1;
   unpack2(z, z0, z1);
-  const float r0 = z0 < 0.0f ? 0.0f : z0, r1 = z1 < 0.0f ? 0.0f : z1;   // (NaN passes)
+  const float r0 = max_nan(z0, 0.0f), r1 = max_nan(z1, 0.0f);
   if (ACT == kActRelu) return pack2(r0, r1);
-  const F32x2 u = pack2(fabsf(z0), fabsf(z1));
+  const F32x2 u = pack2(fminf(fabsf(z0), kGeluCut), fminf(fabsf(z1), kGeluCut));
+  F32x2 q = fma2(u, both(kGelu7), both(kGelu6));
+  q = fma2(q, u, both(kGelu5));
+  q = fma2(q, u, both(kGelu4));
+  q = fma2(q, u, both(kGelu3));
+  q = fma2(q, u, both(kGelu2));
+  q = fma2(q, u, both(kGelu1));
+  q = fma2(q, u, both(kGelu0));
   float a, b;
-  unpack2(fma2(u, both(kGeluC), both(1.0f)), a, b);
-  const F32x2 t = pack2(rcp_approx(a), rcp_approx(b));
-  F32x2 q = fma2(t, both(kGeluP5), both(kGeluP4));
-  q = fma2(q, t, both(kGeluP3));
-  q = fma2(q, t, both(kGeluP2));
-  q = fma2(q, t, both(kGeluP1));
-  q = fma2(q, t, both(kGeluP0));
-  const F32x2 minus_u = pack2(-fabsf(z0), -fabsf(z1));
-  unpack2(mul2(mul2(u, both(0.5f * kLog2e)), minus_u), a, b);
-  q = mul2(mul2(q, t), pack2(ex2_approx(a), ex2_approx(b)));   // Phi(-|z|)
-  return fma2(minus_u, q, pack2(r0, r1));
+  unpack2(q, a, b);
+  q = pack2(ex2_approx(a), ex2_approx(b));               // Phi(-u)
+  return fma2(mul2(u, both(-1.0f)), q, pack2(r0, r1));
 }
 
-// The activation `act` on one value (uniform over the grid: one branch); the
-// same operations as a pair's.
+// The activation `act` on one value (uniform over the grid: one branch), by the
+// same formulas.
 __device__ __forceinline__ float activate(float z, int act) {
   if (act == kActNone) return z;
-  const float r = z < 0.0f ? 0.0f : z;   // (NaN passes)
+  const float r = max_nan(z, 0.0f);
   if (act == kActRelu) return r;
   if (act == kActGelu) {
-    const float u = fabsf(z), t = rcp_approx(fmaf(u, kGeluC, 1.0f));
-    float q = fmaf(t, kGeluP5, kGeluP4);
-    q = fmaf(q, t, kGeluP3);
-    q = fmaf(q, t, kGeluP2);
-    q = fmaf(q, t, kGeluP1);
-    q = fmaf(q, t, kGeluP0);
-    q = __fmul_rn(__fmul_rn(q, t), ex2_approx(__fmul_rn(__fmul_rn(u, 0.5f * kLog2e), -u)));
-    return fmaf(-u, q, r);
+    const float u = fminf(fabsf(z), kGeluCut);
+    float q = fmaf(u, kGelu7, kGelu6);
+    q = fmaf(q, u, kGelu5);
+    q = fmaf(q, u, kGelu4);
+    q = fmaf(q, u, kGelu3);
+    q = fmaf(q, u, kGelu2);
+    q = fmaf(q, u, kGelu1);
+    return fmaf(-u, ex2_approx(fmaf(q, u, kGelu0)), r);
   }
   const float e = act == kActSilu ? __fmul_rn(z, -kLog2e) : __fmul_rn(z, fmaf(__fmul_rn(z, z), kTanh1, kTanh0));
-  return __fmul_rn(z, rcp_approx(__fadd_rn(ex2_approx(e), 1.0f)));
+  return __fmul_rn(z, rcp_approx(__fadd_rn(ex2_approx(fminf(e, kGateCut)), 1.0f)));
 }
 
 }  // namespace fp8q

@@ -251,13 +251,13 @@ fp8q_status launch_gemm(const uint8_t* A, int64_t a_rows, const uint8_t* B, int6
   if (s != FP8Q_OK) return s;
   auto kernel = fp8_gemm_kernel<BN, STAGES, kGrouped, kGather, kEpi>;
   // (kEpi: the dense kernel stages its columns where a grouped one has its schedule)
-  constexpr size_t kEpiSmem = kEpi ? kEpiColBytes + 16 : 0;
+  constexpr size_t kEpiSmem = kEpi ? kEpiColBytes + 16 + (kEpiWarpsFull - kEpiWarps) * kStageTileBytes : 0;
   const size_t smem = L::smem_bytes(kGrouped ? p.E : 0) + kEpiSmem;
   e = ensure_smem<fp8_gemm_kernel<BN, STAGES, kGrouped, kGather, kEpi>>(
       L::smem_bytes(kGrouped ? kMaxExperts : 0) + kEpiSmem, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   const int grid = static_cast<int>(tiles_upper_bound < sms ? (tiles_upper_bound < 1 ? 1 : tiles_upper_bound) : sms);
-  e = launch_ex(kernel, dim3(grid), dim3(kGemmThreads), smem, st, 1, true, ta, tb, ty, p);
+  e = launch_ex(kernel, dim3(grid), dim3(gemm_threads(kEpi)), smem, st, 1, true, ta, tb, ty, p);
   if (e != cudaSuccess) return cuda_fail(e, "fp8_gemm_kernel launch");
   return FP8Q_OK;
 }
@@ -384,7 +384,7 @@ fp8q_status launch_pair(const uint8_t* A, const uint8_t* B, int64_t b_rows, cons
       L::smem_bytes(kGrouped ? kMaxExperts : 0) + kEpiSmem, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(pair)");
   const int pairs = static_cast<int>(tiles < clusters ? (tiles < 1 ? 1 : tiles) : clusters);
-  e = launch_ex(kernel, dim3(2 * pairs), dim3(kGemmThreads), L::smem_bytes(kGrouped ? p.E : 0) + kEpiSmem, st, 2, true, ta, tah,
+  e = launch_ex(kernel, dim3(2 * pairs), dim3(gemm_threads(kEpi)), L::smem_bytes(kGrouped ? p.E : 0) + kEpiSmem, st, 2, true, ta, tah,
                 tb, tbt, ty, p);
   if (e != cudaSuccess) return cuda_fail(e, "fp8_gemm_pair_kernel launch");
   return FP8Q_OK;

@@ -21,6 +21,11 @@ constexpr int kUmmaK = 32;        // K per tcgen05.mma for 8-bit operands
 constexpr int kEpiWarp0 = 2;      // warps 0, 1: TMA producer, MMA issuer
 constexpr int kEpiWarps = 8;      // two epilogue warps per TMEM lane quadrant
 constexpr int kGemmThreads = (kEpiWarp0 + kEpiWarps) * 32;
+// With bias, activation and residual in the epilogue (kEpi): four warps per TMEM
+// lane quadrant, one staging tile each.
+constexpr int kEpiWarpsFull = 16;
+constexpr int epi_warps(bool epi) { return epi ? kEpiWarpsFull : kEpiWarps; }
+constexpr int gemm_threads(bool epi) { return (kEpiWarp0 + epi_warps(epi)) * 32; }
 constexpr int kStageTileBytes = 32 * 32 * 2;   // one 32 x 32 fp16 output tile per epilogue warp
 // Staging for kBufs tiles per epilogue warp: buffer b of warp w at
 // (b * kEpiWarps + w) * kStageTileBytes.
@@ -135,7 +140,7 @@ struct EpiScales {
   int ctok;    // combine: output (token) row of this lane's row, -1: none
 };
 
-template <int kMaxChunks, bool kEpi = false>
+template <int kMaxChunks>
 __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& t, const GemmParams& p,
                                                                  const EpiWarpView& w, int lane) {
   EpiScales<kMaxChunks> e;
@@ -157,7 +162,7 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
 #pragma unroll
   for (int j = 0; j < kMaxChunks; ++j) {
     const int cl = w.col0 + j * 32 + lane;
-    if (!kEpi) e.sw[j] = (j < w.nch && t.n0 + cl < p.N) ? __ldg(p.s_w + t.sw0 + cl) : 0.0f;
+    e.sw[j] = (j < w.nch && t.n0 + cl < p.N) ? __ldg(p.s_w + t.sw0 + cl) : 0.0f;
   }
   return e;
 }
@@ -168,8 +173,8 @@ __device__ __forceinline__ EpiScales<kMaxChunks> epilogue_scales(const EpiTile& 
 // fp32 and rounded to nearest; one rounding to fp16.
 //
 // What it needs besides the accumulators:
-//   * s_w and the bias of the tile's columns, which the four warps of a column half
-//     stage in shared memory while the tile's MMAs run, and all lanes read at the
+//   * s_w and the bias of the tile's columns, which the epilogue warps stage in
+//     shared memory while the tile's MMAs run, and all lanes read at the
 //     same address (one 16-byte read for four scales or eight biases, where handing
 //     them round by shuffles takes an instruction a column);
 //   * the residual of the chunk's 32 x 32 values, loaded a chunk ahead four lanes to
@@ -187,23 +192,45 @@ __device__ __forceinline__ EpiCols epi_cols(void* after_bars) {
   return c;
 }
 
-// Stage the columns of one half (h = 0 or 1) of a bn-wide tile: called by the
-// half's four warps (named barrier 2 + h, 128 threads) before they wait for the
-// accumulator; the first barrier ends their reads of the tile before.
-__device__ __forceinline__ void epilogue_stage_columns(const EpiCols& c, const GemmParams& p, int n0, int bn, int warp,
-                                                       int lane) {
-  const int h = (warp - kEpiWarp0) >> 2;
-  const int i = (warp & 3) * 32 + lane;
-  const int col = h * (bn / 2) + i;
-  const bool mine = i < bn / 2, in = mine && n0 + col < p.N;
-  const float w = in ? __ldg(p.s_w + n0 + col) : 0.0f;
-  const __half b = in && p.bias != nullptr ? __ldg(p.bias + n0 + col) : __float2half_rn(0.0f);
-  named_barrier(2 + h, 128);
-  if (mine) {
-    c.w[col] = w;
-    c.b[col] = b;
+// What a kEpi epilogue warp does next: its rows of the tile and the values that
+// it loads while the tile before is drained, so that no load's latency stands
+// between two tiles.
+struct EpiNext {
+  int n0, bn;        // the tile's columns
+  int row0, valid;   // first row of the warp's TMEM lane quadrant, rows that are stored
+  float sx;          // scale of the lane's row
+  float w;           // scale and bias of column threadIdx.x of the epilogue threads
+  __half b;
+};
+// slab0: first of the CTA's 128 rows.
+__device__ __forceinline__ EpiNext epilogue_next(const GemmParams& p, int n0, int bn, int slab0, int row_end) {
+  const int tid = threadIdx.x - kEpiWarp0 * 32, lane = tid & 31;
+  EpiNext e;
+  e.n0 = n0;
+  e.bn = bn;
+  e.row0 = slab0 + ((threadIdx.x >> 5) & 3) * 32;
+  e.valid = row_end - e.row0;
+  e.sx = lane < e.valid ? __ldg(p.s_x + e.row0 + lane) : 0.0f;
+  const bool in = tid < bn && n0 + tid < p.N;
+  e.w = in ? __ldg(p.s_w + n0 + tid) : 0.0f;
+  e.b = in && p.bias != nullptr ? __ldg(p.bias + n0 + tid) : __float2half_rn(0.0f);
+  // The tile's residual to L2 (128 rows x 512 bytes, a 128-byte line a thread): a
+  // chunk's loads are issued one chunk ahead, which covers L2's latency and not HBM's.
+  const int r = tid >> 2, c = (tid & 3) * 64;
+  if (p.residual != nullptr && c < bn && n0 + c < p.N && slab0 + r < row_end)
+    prefetch_l2(p.residual + static_cast<int64_t>(slab0 + r) * p.N + n0 + c);
+  return e;
+}
+
+// Stage a tile's columns: all kEpi epilogue threads (named barrier 2), before they
+// wait for the accumulator; the first barrier ends their reads of the tile before.
+__device__ __forceinline__ void epilogue_stage_columns(const EpiCols& c, const EpiNext& e, int tid) {
+  named_barrier(2, kEpiWarpsFull * 32);
+  if (tid < e.bn) {
+    c.w[tid] = e.w;
+    c.b[tid] = e.b;
   }
-  named_barrier(2 + h, 128);
+  named_barrier(2, kEpiWarpsFull * 32);
 }
 
 // Residual of a chunk (32 rows from row0, 32 columns from n), four lanes to a row:
@@ -218,12 +245,12 @@ __device__ __forceinline__ void epilogue_residual(uint4 (&r)[4], const GemmParam
 }
 
 template <int ACT>
-__device__ __forceinline__ void activate_pairs(F32x2 (&z)[16]) {
+__device__ __forceinline__ void activate_pairs(F32x2 (&z)[8]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = activate2<ACT>(z[i]);
+  for (int i = 0; i < 8; ++i) z[i] = activate2<ACT>(z[i]);
 }
 
-__device__ __forceinline__ void activate_pairs_any(F32x2 (&z)[16], int act) {
+__device__ __forceinline__ void activate_pairs_any(F32x2 (&z)[8], int act) {
   switch (act) {   // uniform
     case kActRelu: activate_pairs<kActRelu>(z); break;
     case kActGelu: activate_pairs<kActGelu>(z); break;
@@ -233,95 +260,94 @@ __device__ __forceinline__ void activate_pairs_any(F32x2 (&z)[16], int act) {
   }
 }
 
-// epilogue_slab (below) with bias, activation and residual.  `cols`: the tile's
-// staged columns; `res`: the residual of the warp's first chunk (a chunk's
-// residual is read before the same warp stores the chunk, so it may be Y itself).
-// The chunk loop stays rolled and the activations are the only code that is there
-// once for each kind: unrolled like the plain slab it ran out of the instruction
-// cache (4096 x 8192 x 1024 with GELU: 63 us).  Once a chunk is scaled its
-// accumulator registers take the TMEM load of the next, in flight during the
-// activation.
-template <int kBufs>
-__device__ __forceinline__ void epilogue_slab_epi(const EpiTile& t, const GemmParams& p, const CUtensorMap* tmY,
-                                                  uint32_t tmem_acc, const EpiWarpView& w, int warp, int lane,
-                                                  uint8_t* stage, float sx, const EpiCols& cols, uint4 (&res)[4]) {
-  const int q = warp & 3;
-  const int valid = t.row_end - w.qrow0;   // rows of this warp that are stored (<= 0: none)
-  if (valid <= 0) return;
-  const uint32_t taddr0 = tmem_acc + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(w.tcol0);
-  const F32x2 sx2 = both(sx);
-  uint32_t v[32];
-  tmem_ld_32x32b_x32(taddr0, v);
-  if (kBufs == 2 && lane == 0) bulk_wait_read_all();
+// One kEpi epilogue warp drains its share of a tile of bn columns: rows of its TMEM
+// lane quadrant (warp % 4), 32-column chunks h, h + 4, .. for its h of four (bn / 32
+// chunks, two to eight).  `cols`: the tile's staged columns; `res`: the residual of
+// the warp's first chunk, and on return of its first chunk of the tile `next`
+// (every value of the residual is read by the warp that stores the output in its place,
+// before it does, so the residual may be Y itself).
+// What bounds it is issue latency, so there are four warps a scheduler, a chunk
+// goes through in two halves of 16 columns to fit their registers, and the chunk and
+// half loops stay rolled: unrolled like the plain slab the code ran out of the
+// instruction cache.  4096 x 8192 x 1024 with bias and GELU, where the epilogue is
+// longer than the mainloop: 63 us unrolled, 55 rolled (eight warps, whole chunks).
+__device__ __forceinline__ void epilogue_slab_epi(const GemmParams& p, const CUtensorMap* tmY, uint32_t tmem_acc,
+                                                  const EpiNext& t, const EpiNext& next, int warp, int lane,
+                                                  uint8_t* stage, const EpiCols& cols, uint4 (&res)[4]) {
+  const int h32 = ((warp - kEpiWarp0) >> 2) * 32;   // first column of the warp's first chunk
+  const uint32_t taddr = tmem_acc + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const F32x2 sx2 = both(t.sx);
+  const uint32_t sbase = smem_u32(stage);
 #pragma unroll 1
-  for (int j = 0; j < w.nch; ++j) {
-    const int cl = w.col0 + j * 32;   // first column of the chunk within the tile
-    uint8_t* buf = stage + (kBufs == 2 ? (j & 1) * kEpiWarps * kStageTileBytes : 0);
-    const uint32_t sbase = smem_u32(buf);
-    // the staging tile must have been read by its last bulk store
-    if (lane == 0) {
-      if (kBufs == 2) bulk_wait_read_1();
-      else bulk_wait_read_all();
-    }
+  for (int cl = h32; cl < t.bn && t.valid > 0; cl += 128) {   // first column of the chunk
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(cl), v);
+    if (lane == 0) bulk_wait_read_all();   // the staging tile has been read by its last bulk store
     __syncwarp();
     if (p.residual != nullptr) {
 #pragma unroll
       for (int it = 0; it < 4; ++it)
         st_shared_v4(sbase + stage_off(it * 8 + (lane >> 2), lane & 3), res[it].x, res[it].y, res[it].z, res[it].w);
-      if (j + 1 < w.nch) epilogue_residual(res, p, w.qrow0, valid, t.n0 + cl + 32, lane);
+      __syncwarp();
+      if (cl + 128 < t.bn) epilogue_residual(res, p, t.row0, t.valid, t.n0 + cl + 128, lane);
+      else if (h32 < next.bn) epilogue_residual(res, p, next.row0, next.valid, next.n0 + h32, lane);
     }
-    F32x2 z[16];
     tmem_ld_wait_regs(v);
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float4 s = *reinterpret_cast<const float4*>(cols.w + cl + 2 * i);
-      z[i] = mul2(mul2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sx2), pack2(s.x, s.y));
-      z[i + 1] = mul2(mul2(pack2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), sx2), pack2(s.z, s.w));
-    }
-    if (p.bias != nullptr) {   // uniform, as the branches below
+    for (int h = 0; h < 2; ++h) {
+      F32x2 z[8];
+      const float* w = cols.w + cl + 16 * h;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const uint4 b = *reinterpret_cast<const uint4*>(cols.b + cl + 2 * i);
+      for (int i = 0; i < 8; i += 2) {
+        const float4 s = *reinterpret_cast<const float4*>(w + 2 * i);
+        const uint32_t* a = v + 16 * h + 2 * i;
+        z[i] = mul2(mul2(pack2(__uint_as_float(a[0]), __uint_as_float(a[1])), sx2), pack2(s.x, s.y));
+        z[i + 1] = mul2(mul2(pack2(__uint_as_float(a[2]), __uint_as_float(a[3])), sx2), pack2(s.z, s.w));
+      }
+      if (p.bias != nullptr) {   // uniform, as the branches below
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(reinterpret_cast<const __half2*>(&b)[k]);
-          z[i + k] = add2(z[i + k], pack2(f.x, f.y));
+        for (int i = 0; i < 8; i += 4) {
+          const uint4 b = *reinterpret_cast<const uint4*>(cols.b + cl + 16 * h + 2 * i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(reinterpret_cast<const __half2*>(&b)[k]);
+            z[i + k] = add2(z[i + k], pack2(f.x, f.y));
+          }
         }
       }
-    }
-    if (j + 1 < w.nch) tmem_ld_32x32b_x32(taddr0 + static_cast<uint32_t>((j + 1) * 32), v);
-    activate_pairs_any(z, p.act);
-    if (p.residual != nullptr) {
-      __syncwarp();
+      activate_pairs_any(z, p.act);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 r = ld_shared_v4(sbase + stage_off(lane, c));
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t at = sbase + stage_off(lane, 2 * h + c);
+        if (p.residual != nullptr) {
+          const uint4 r = ld_shared_v4(at);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(reinterpret_cast<const __half2*>(&r)[k]);
+            z[4 * c + k] = add2(z[4 * c + k], pack2(f.x, f.y));
+          }
+        }
+        uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(reinterpret_cast<const __half2*>(&r)[k]);
-          z[4 * c + k] = add2(z[4 * c + k], pack2(f.x, f.y));
+          float a, b;
+          unpack2(z[4 * c + k], a, b);
+          const __half2 hv = __floats2half2_rn(a, b);
+          o[k] = *reinterpret_cast<const uint32_t*>(&hv);
         }
+        st_shared_v4(at, o[0], o[1], o[2], o[3]);
       }
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a, b;
-        unpack2(z[4 * c + k], a, b);
-        const __half2 hv = __floats2half2_rn(a, b);
-        h[k] = *reinterpret_cast<const uint32_t*>(&hv);
-      }
-      st_shared_v4(sbase + stage_off(lane, c), h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(tmY, buf, t.n0 + cl, w.qrow0);   // dense: rows past the end lie past the tensor
+      tma_store_2d(tmY, stage, t.n0 + cl, t.row0);   // dense: rows past the end lie past the tensor
       bulk_commit_group();
     }
   }
+  // a warp that had nothing to drain in this tile
+  if (p.residual != nullptr && (t.valid <= 0 || h32 >= t.bn) && h32 < next.bn)
+    epilogue_residual(res, p, next.row0, next.valid, next.n0 + h32, lane);
 }
 
 // One epilogue warp drains its view (above), 32 columns at a time:

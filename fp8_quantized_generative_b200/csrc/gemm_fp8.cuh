@@ -100,7 +100,7 @@ __device__ __forceinline__ TileCoord decode_tile(int t, const GemmParams& p, int
 }
 
 template <int BN, int STAGES, bool kGrouped, bool kGather = false, bool kEpi = false>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(kEpi), 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
   using L = GemmLayout<BN, STAGES>;
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   static_assert(!kGather || kGrouped, "gathered rows are a grouped (MoE) form");
   constexpr int kGatherLag = 1;   // stages of row copies in flight before a stage is signalled
   static_assert(!kGather || kGatherLag < STAGES, "lag");
+  static_assert(!kEpi || !kGrouped, "bias, activation and residual are a dense form");
   // A = activations: E4M3, or E5M2 for the activation-format variant
   const uint32_t kIdesc = idesc_e4m3_f32(kBM, BN) | idesc_a_fmt(p.x_fmt);
 
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES * L::kABytes;
   uint8_t* sEpi = sB + STAGES * L::kBBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + epi_smem_bytes(L::kEpiBufs));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + (kEpi ? kEpiWarpsFull * kStageTileBytes : epi_smem_bytes(L::kEpiBufs)));
   uint64_t* full = bars;
   uint64_t* empty = bars + STAGES;
   uint64_t* tfull = bars + 2 * STAGES;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kEpiWarps);
+      mbar_init(&tempty[b], epi_warps(kEpi));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -351,37 +352,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // ------------------------------------------------------------ epilogue
     uint8_t* stage = sEpi + (warp - kEpiWarp0) * kStageTileBytes;
     const EpiCols cols = kEpi ? epi_cols(tile_prefix) : EpiCols{};
-    uint4 res[4];   // kEpi: residual of the next chunk
+    uint4 res[4];   // kEpi: residual of the warp's next chunk
+    EpiNext next = {};
+    auto next_tile = [&](int tt) {   // kEpi: tile tt (past the last: no columns)
+      const TileCoord c = decode_tile<kGrouped, BN>(min(tt, total - 1), p, num_m, num_n, tile_prefix, offs);
+      return epilogue_next(p, c.n0, tt < total ? BN : 0, c.a_row0, c.row_end);
+    };
+    if constexpr (kEpi) {
+      next = next_tile(static_cast<int>(blockIdx.x));
+      const int h32 = ((warp - kEpiWarp0) >> 2) * 32;
+      if (p.residual != nullptr && h32 < next.bn) epilogue_residual(res, p, next.row0, next.valid, next.n0 + h32, lane);
+    }
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       const TileCoord c = decode_tile<kGrouped, BN>(t, p, num_m, num_n, tile_prefix, offs);
-      EpiTile et;
-      et.row0 = c.a_row0;
-      et.row_end = c.row_end;
-      et.n0 = c.n0;
-      et.sw0 = c.sw0;
-      et.clip = !kGrouped;   // dense: rows past the end are past the tensor
-      const EpiWarpView wv = epi_view(et, warp, BN, false);
-      const EpiScales<BN / 64> sc = epilogue_scales<BN / 64, kEpi>(et, p, wv, lane);
       if constexpr (kEpi) {
-        epilogue_stage_columns(cols, p, c.n0, BN, warp, lane);
-        if (p.residual != nullptr)
-          epilogue_residual(res, p, wv.qrow0, c.row_end - wv.qrow0, c.n0 + wv.col0, lane);
-      }
-      if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
-        raise_error(0x4u);
-        *abort_flag = 1;
-        if constexpr (kEpi) continue;   // the warps of a column half meet at barriers: all walk on
-        break;
-      }
-      tc_fence_after();
-      if constexpr (kEpi)
-        epilogue_slab_epi<L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp,
-                                                lane, stage, sc.sx, cols, res);
-      else
+        const EpiNext cur = next;
+        next = next_tile(t + static_cast<int>(gridDim.x));
+        epilogue_stage_columns(cols, cur, threadIdx.x - kEpiWarp0 * 32);
+        if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
+          raise_error(0x4u);
+          *abort_flag = 1;
+          continue;   // the epilogue warps meet at barriers: all walk on
+        }
+        tc_fence_after();
+        epilogue_slab_epi(p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), cur, next, warp, lane, stage, cols, res);
+      } else {
+        EpiTile et;
+        et.row0 = c.a_row0;
+        et.row_end = c.row_end;
+        et.n0 = c.n0;
+        et.sw0 = c.sw0;
+        et.clip = !kGrouped;   // dense: rows past the end are past the tensor
+        const EpiWarpView wv = epi_view(et, warp, BN, false);
+        const EpiScales<BN / 64> sc = epilogue_scales<BN / 64>(et, p, wv, lane);
+        if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
+          raise_error(0x4u);
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
         epilogue_slab<BN / 64, L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
                                             stage, sc);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[acc]);

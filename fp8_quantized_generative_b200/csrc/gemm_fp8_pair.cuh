@@ -123,7 +123,7 @@ __device__ __forceinline__ PairTile pair_tile(int t, const GemmParams& p, int nu
 
 // kEpi (dense): bias, activation and residual in the epilogue.
 template <int BN, int STAGES, bool kGrouped, bool kQuantA = false, int SK = kBK, bool kEpi = false>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(kEpi), 1)
     fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAh,
                          const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBt,
                          const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kEpiWarps);   // one arrival per epilogue warp of both CTAs
+      mbar_init(&tempty[b], 2 * epi_warps(kEpi));   // one arrival per epilogue warp of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -401,7 +401,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     uint8_t* stage = sEpi + (warp - kEpiWarp0) * kStageTileBytes;
     const EpiCols cols = kEpi ? epi_cols(tile_prefix) : EpiCols{};
-    uint4 res[4];   // kEpi: residual of the next chunk
+    uint4 res[4];   // kEpi: residual of the warp's next chunk
+    EpiNext next = {};
+    auto next_tile = [&](int tt) {   // kEpi: tile tt (past the last: no columns)
+      const PairTile pt = pair_tile<BN, kGrouped>(min(tt, total - 1), p, num_m, num_n, tile_prefix, offs);
+      return epilogue_next(p, pt.n0, tt < total ? pt.bn : 0, pt.a_row0 + static_cast<int>(rank) * kBM, pt.row_end);
+    };
+    if constexpr (kEpi) {
+      next = next_tile(static_cast<int>(pair));
+      const int h32 = ((warp - kEpiWarp0) >> 2) * 32;
+      if (p.residual != nullptr && h32 < next.bn) epilogue_residual(res, p, next.row0, next.valid, next.n0 + h32, lane);
+    }
     const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
     int acc = 0;
@@ -409,43 +419,46 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     RowsReady ready;
     for (int t = pair; t < total; t += npairs) {
       const PairTile pt = pair_tile<BN, kGrouped>(t, p, num_m, num_n, tile_prefix, offs);
-      EpiTile et;
-      et.row0 = pt.a_row0 + static_cast<int>(rank) * (pt.half ? kBM / 2 : kBM);
-      et.row_end = pt.row_end;
-      et.n0 = pt.n0;
-      et.sw0 = pt.sw0;
-      et.clip = !kGrouped;   // dense: rows past the end are past the tensor
-      const EpiWarpView wv = epi_view(et, warp, pt.bn, pt.half);
-      EpiScales<BN / 64> sc = epilogue_scales<BN / 64, kEpi>(et, p, wv, lane);
-      if (kQuantA) {
-        // the row scales were written in this kernel: read them once the
-        // block is complete (it is before its first MMA, so this wait ends)
-        if (!ready.wait(p, et.row0, false)) {
+      if constexpr (kEpi) {
+        const EpiNext cur = next;
+        next = next_tile(t + static_cast<int>(npairs));
+        epilogue_stage_columns(cols, cur, threadIdx.x - kEpiWarp0 * 32);
+        if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
+          raise_error(0x4u);
+          *abort_flag = 1;
+          continue;   // the epilogue warps meet at barriers: all walk on
+        }
+        tc_fence_after();
+        epilogue_slab_epi(p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), cur, next, warp, lane, stage, cols, res);
+      } else {
+        EpiTile et;
+        et.row0 = pt.a_row0 + static_cast<int>(rank) * (pt.half ? kBM / 2 : kBM);
+        et.row_end = pt.row_end;
+        et.n0 = pt.n0;
+        et.sw0 = pt.sw0;
+        et.clip = !kGrouped;   // dense: rows past the end are past the tensor
+        const EpiWarpView wv = epi_view(et, warp, pt.bn, pt.half);
+        EpiScales<BN / 64> sc = epilogue_scales<BN / 64>(et, p, wv, lane);
+        if (kQuantA) {
+          // the row scales were written in this kernel: read them once the
+          // block is complete (it is before its first MMA, so this wait ends)
+          if (!ready.wait(p, et.row0, false)) {
+            raise_error(0x4u);
+            *abort_flag = 1;
+            break;
+          }
+          const int r = wv.qrow0 + lane;
+          sc.sx = r < et.row_end ? ld_relaxed_gpu_f32(p.s_x + r) : 0.0f;
+        }
+        if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
           raise_error(0x4u);
           *abort_flag = 1;
           break;
         }
-        const int r = wv.qrow0 + lane;
-        sc.sx = r < et.row_end ? ld_relaxed_gpu_f32(p.s_x + r) : 0.0f;
-      }
-      if constexpr (kEpi) {
-        epilogue_stage_columns(cols, p, pt.n0, pt.bn, warp, lane);
-        if (p.residual != nullptr)
-          epilogue_residual(res, p, wv.qrow0, pt.row_end - wv.qrow0, pt.n0 + wv.col0, lane);
-      }
-      if (!mbar_wait(&tfull[acc], acc_ph, abort_flag)) {
-        raise_error(0x4u);
-        *abort_flag = 1;
-        if constexpr (kEpi) continue;   // the warps of a column half meet at barriers: all walk on
-        break;
-      }
-      tc_fence_after();
-      if constexpr (kEpi)
-        epilogue_slab_epi<L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp,
-                                                lane, stage, sc.sx, cols, res);
-      else
+        tc_fence_after();
         epilogue_slab<BN / 64, L::kEpiBufs>(et, p, &tmY, tmem_base + static_cast<uint32_t>(acc * BN), wv, warp, lane,
                                             stage, sc);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);

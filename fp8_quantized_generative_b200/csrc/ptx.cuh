@@ -431,6 +431,8 @@ __device__ __forceinline__ uint4 ld_global_v4(const void* ptr) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
+
 __device__ __forceinline__ uint32_t ld_global_u32(const void* ptr) {
   uint32_t v;
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
