@@ -58,6 +58,7 @@ constexpr int kMfThreads = kMfConsumers + kMfEpiThreads + 32;   // + the warp th
 constexpr int kMfMaxRows = 1024;       // T * topk
 constexpr int kMfMaxTopk = 8;
 constexpr int kMfMaxExperts = 1024;
+constexpr int kMfFuseTokens = 8;
 constexpr int kMfStageBytes = 32768;   // RU weight rows x 32 KB / RU of K
 constexpr int kMfMaxStages = 6;
 constexpr int kMfMaxSmem = 232448;     // 227 KB
@@ -74,6 +75,13 @@ struct MoeFewParams {
   int act;                  // up: Activation
   __half* hidden;           // up: [T * topk, F]
   float* y;                 // down: [T * topk, N]
+  // With at most kMfFuseTokens tokens and two units a CTA the down projection also
+  // adds the tokens' rows up (done != nullptr); else moe_few_combine_kernel does.
+  uint32_t* done;           // a counter a unit of the down projection, zeroed by the up projection
+  int done_units;
+  const float* weights;     // [T * topk]
+  const __half* residual;   // [T, N] or nullptr
+  __half* out;              // [T, N]
   int rmax;                 // rows of a segment, a multiple of 8
   int units;                // of a segment
   int stages;               // of the ring
@@ -285,6 +293,26 @@ __device__ __forceinline__ void mf_build_rows(const MoeFewParams& p, int seg, co
   }
 }
 
+// The weighted sum of a token's rows, in the order of its choices, + residual, rounded once.
+__device__ __forceinline__ void mf_add_weighted(float4& a, float w, const float4& v) {
+  a.x = fmaf(w, v.x, a.x);
+  a.y = fmaf(w, v.y, a.y);
+  a.z = fmaf(w, v.z, a.z);
+  a.w = fmaf(w, v.w, a.w);
+}
+__device__ __forceinline__ void mf_store_out(const __half* residual, __half* out, int64_t at, float4 a) {
+  if (residual != nullptr) {
+    const __half2* r = reinterpret_cast<const __half2*>(residual + at);
+    const float2 r0 = __half22float2(r[0]), r1 = __half22float2(r[1]);
+    a.x += r0.x;
+    a.y += r0.y;
+    a.z += r1.x;
+    a.w += r1.y;
+  }
+  __half2 h[2] = {__floats2half2_rn(a.x, a.y), __floats2half2_rn(a.z, a.w)};
+  *reinterpret_cast<uint2*>(out + at) = *reinterpret_cast<const uint2*>(h);
+}
+
 // NT: n-tiles of 8 rows a segment may have; MT: 16-row weight tiles of a unit (RU =
 // 16 MT).  tmW: the weights [E * wrows, K] in boxes of 128 bytes x RU rows (gated:
 // RU / 2).
@@ -307,6 +335,7 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
   uint64_t* pfull = empty + kMfMaxStages;
   uint64_t* pempty = pfull + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(pempty + 2);
+  volatile int* last_flag = abort_flag + 1;
   int* rows = reinterpret_cast<int*>(mf_smem + L.rows);
   int* segs = reinterpret_cast<int*>(mf_smem + L.segs);
   int* counts = reinterpret_cast<int*>(mf_smem + L.counts);
@@ -330,6 +359,8 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
   if (kUp) {
     pdl_wait_prior_grid();
     pdl_launch_dependents();
+    if (p.done != nullptr && blockIdx.x == gridDim.x - 1)
+      for (int i = threadIdx.x; i < p.done_units; i += kMfThreads) p.done[i] = 0;
   }
   const int nseg = mf_schedule(p, rows, segs, counts, reinterpret_cast<int*>(part), kUp && blockIdx.x == 0);
   const int nu = p.units;                           // units of a segment
@@ -401,6 +432,39 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
     // (the stores come after the wait below and the partials' first barrier: behind
     // the kernel before this one, as the multiplying warps wait for it)
     const int tid = threadIdx.x - kMfConsumers;
+    // Adding up (one n-tile: at most 8 tokens): this thread's token, four columns of
+    // the unit, and what it needs of the router, loaded ahead.
+    constexpr bool kFuse = !kUp && NT == 1;
+    constexpr int kVec = outs / 4;
+    static_assert(kMfFuseTokens * kVec <= kMfEpiThreads, "a thread an item");
+    const int ct = tid / kVec, cn = (tid % kVec) * 4;
+    const bool adds = kFuse && p.done != nullptr && ct * p.topk < p.rows;
+    float cw[kMfMaxTopk];
+    uint32_t has = 0;   // choices with an expert
+    if (adds) {
+#pragma unroll
+      for (int j = 0; j < kMfMaxTopk; ++j) {
+        if (j < p.topk) {
+          const int e = __ldg(p.experts + ct * p.topk + j);
+          cw[j] = __ldg(p.weights + ct * p.topk + j);
+          has |= static_cast<uint32_t>(e >= 0 && e < p.E) << j;
+        }
+      }
+    }
+    auto add_up = [&](int n0) {   // columns n0 .. n0 + outs - 1 of every token
+      const int n = n0 + cn;
+      if (!adds || n >= p.n_out) return;
+      const float* y = p.y + static_cast<int64_t>(ct) * p.topk * p.n_out + n;
+      float4 v[kMfMaxTopk];
+#pragma unroll
+      for (int j = 0; j < kMfMaxTopk; ++j)
+        if (has >> j & 1u) v[j] = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(j) * p.n_out));
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < kMfMaxTopk; ++j)
+        if (has >> j & 1u) mf_add_weighted(a, cw[j], v[j]);
+      mf_store_out(p.residual, p.out, static_cast<int64_t>(ct) * p.n_out + n, a);
+    };
     constexpr int step = kMfEpiThreads / outs;
     const int u = tid & (outs - 1), r1 = tid / outs;
     for (int s = s_first, k3 = 0; s * nu < hi; ++s, k3 = k3 == 2 ? 0 : k3 + 1) {
@@ -445,7 +509,19 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
           buf = 0;
           bph ^= 1u;
         }
+        if (kFuse && p.done != nullptr) {
+          // the CTA that brings the last segment's rows of these columns adds them up
+          named_barrier(3, kMfEpiThreads);
+          if (tid == 0)
+            *last_flag = atom_add_acq_rel_gpu(p.done + (unit - s * nu), 1u) == static_cast<uint32_t>(nseg - 1);
+          named_barrier(3, kMfEpiThreads);
+          if (*last_flag) add_up(n - u);
+        }
       }
+    }
+    if (kFuse && p.done != nullptr && nseg == 0) {   // no token has an expert: residual or zero
+      pdl_wait_prior_grid();
+      for (int c = static_cast<int>(blockIdx.x) * outs; c < p.n_out; c += static_cast<int>(gridDim.x) * outs) add_up(c);
     }
     return;
   }
@@ -576,22 +652,9 @@ __global__ void __launch_bounds__(256) moe_few_combine_kernel(const float* y, co
       if (e < 0 || e >= E) continue;
       const float w = __ldg(weights + t * topk + j);
       const float4 v = *reinterpret_cast<const float4*>(y + static_cast<int64_t>(t * topk + j) * N + c);
-      a.x = fmaf(w, v.x, a.x);
-      a.y = fmaf(w, v.y, a.y);
-      a.z = fmaf(w, v.z, a.z);
-      a.w = fmaf(w, v.w, a.w);
+      mf_add_weighted(a, w, v);
     }
-    const int64_t at = static_cast<int64_t>(t) * N + c;
-    if (residual != nullptr) {
-      const __half2* r = reinterpret_cast<const __half2*>(residual + at);
-      const float2 r0 = __half22float2(r[0]), r1 = __half22float2(r[1]);
-      a.x += r0.x;
-      a.y += r0.y;
-      a.z += r1.x;
-      a.w += r1.y;
-    }
-    __half2 h[2] = {__floats2half2_rn(a.x, a.y), __floats2half2_rn(a.z, a.w)};
-    *reinterpret_cast<uint2*>(out + at) = *reinterpret_cast<const uint2*>(h);
+    mf_store_out(residual, out, static_cast<int64_t>(t) * N + c, a);
   }
 }
 

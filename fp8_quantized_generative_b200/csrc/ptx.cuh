@@ -414,6 +414,13 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu_u32(const uint32_t* ptr) {
 __device__ __forceinline__ void st_release_gpu_u32(uint32_t* ptr, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(ptr), "r"(v) : "memory");
 }
+// Atomic add that releases this thread's (and, through barriers, its CTA's) writes
+// before it and acquires those of the threads whose adds it follows; returns the old value.
+__device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* ptr, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(ptr), "r"(v) : "memory");
+  return old;
+}
 __device__ __forceinline__ float ld_relaxed_gpu_f32(const float* ptr) {
   float v;
   asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(ptr) : "memory");
