@@ -26,7 +26,8 @@
 // Work: the chosen experts, each cut into segments of at most rmax rows; a segment
 // is a run of units of `outs` outputs (RU = 16, 32 or 64 weight rows; gated: half of
 // them from each half of the up projection).  Every CTA takes an equal share of
-// the units of all segments.  Its warps:
+// the units of all segments, where a segment's start counts as so many units more as
+// its quantization costs.  Its warps:
 //   0..7    quantize a segment's rows into shared memory, then multiply: each takes
 //           an eighth of a stage's K for all rows of the unit and leaves its partial
 //           sums of the unit in shared memory;
@@ -84,6 +85,7 @@ struct MoeFewParams {
   __half* out;              // [T, N]
   int rmax;                 // rows of a segment, a multiple of 8
   int units;                // of a segment
+  int lead;                 // places before a segment's units that stand for its quantization in the equal shares
   int stages;               // of the ring
 };
 
@@ -364,11 +366,15 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
   }
   const int nseg = mf_schedule(p, rows, segs, counts, reinterpret_cast<int*>(part), kUp && blockIdx.x == 0);
   const int nu = p.units;                           // units of a segment
-  const int total = nseg * nu;
+  const int width = nu + p.lead;                    // places of a segment: its lead (no work), then its units
+  const int total = nseg * width;
   const int share = total / static_cast<int>(gridDim.x), more = total - share * static_cast<int>(gridDim.x);
   const int lo = share * static_cast<int>(blockIdx.x) + min(static_cast<int>(blockIdx.x), more);
   const int hi = lo + share + (static_cast<int>(blockIdx.x) < more ? 1 : 0);
-  const int s_first = lo < hi ? lo / nu : nseg;     // first segment
+  const int s_first = lo < hi ? lo / width : nseg;  // first segment
+  // units [first, end) of segment s in this share
+  auto seg_first = [&](int s) { return max(lo - s * width - p.lead, 0); };
+  auto seg_end = [&](int s) { return min(hi - s * width - p.lead, nu); };
   const int boxes = (p.K + 127) / 128;              // 128-byte boxes of K
   constexpr int stage_boxes = 16 / MT;
   const int wrows = kHalves * p.n_out;
@@ -379,36 +385,32 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
       int slot = 0;
       uint32_t ph = 0, armed = 0, armed_ph = 0;
       bool ok = true;
-      int s = s_first;
-      int n0 = (lo - s * nu) * outs;
-      for (int i = lo; i < hi && ok; ++i) {
-        const int row = mf_seg_expert(segs[s]) * wrows + n0;
-        for (int b0 = 0; b0 < boxes; b0 += stage_boxes) {
-          const int nbox = min(stage_boxes, boxes - b0);
-          if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(nbox * RU * 128));
-          uint8_t* dst = ring + slot * kMfStageBytes;
-          for (int b = 0; b < nbox; ++b) {
+      for (int s = s_first; s * width < hi && ok; ++s) {
+        const int end = seg_end(s);
+        for (int unit = seg_first(s); unit < end && ok; ++unit) {
+          const int row = mf_seg_expert(segs[s]) * wrows + unit * outs;
+          for (int b0 = 0; b0 < boxes; b0 += stage_boxes) {
+            const int nbox = min(stage_boxes, boxes - b0);
+            if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(nbox * RU * 128));
+            uint8_t* dst = ring + slot * kMfStageBytes;
+            for (int b = 0; b < nbox; ++b) {
 #pragma unroll
-            for (int q = 0; q < kHalves; ++q) {
-              tma_load_2d(dst, &tmW, &full[slot], (b0 + b) * 128, row + q * p.n_out);
-              dst += outs * 128;
+              for (int q = 0; q < kHalves; ++q) {
+                tma_load_2d(dst, &tmW, &full[slot], (b0 + b) * 128, row + q * p.n_out);
+                dst += outs * 128;
+              }
+            }
+            armed |= 1u << slot;
+            armed_ph = (armed_ph & ~(1u << slot)) | (ph << slot);
+            if (++slot == p.stages) {
+              slot = 0;
+              ph ^= 1u;
             }
           }
-          armed |= 1u << slot;
-          armed_ph = (armed_ph & ~(1u << slot)) | (ph << slot);
-          if (++slot == p.stages) {
-            slot = 0;
-            ph ^= 1u;
-          }
-        }
-        n0 += outs;
-        if (n0 >= p.n_out) {
-          n0 = 0;
-          ++s;
         }
       }
       if (!ok) {
@@ -467,14 +469,15 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
     };
     constexpr int step = kMfEpiThreads / outs;
     const int u = tid & (outs - 1), r1 = tid / outs;
-    for (int s = s_first, k3 = 0; s * nu < hi; ++s, k3 = k3 == 2 ? 0 : k3 + 1) {
+    for (int s = s_first, k3 = 0; s * width < hi; ++s) {
+      const int first = seg_first(s), end = seg_end(s);
+      if (first >= end) continue;
       const int seg = segs[s];
       const int e = mf_seg_expert(seg), cnt = mf_seg_count(seg), row0 = mf_seg_row0(seg);
       const int nt = (cnt + 7) >> 3;
       const float* sw = p.s_w + static_cast<int64_t>(e) * wrows + u;
-      const int first = max(lo, s * nu), end = min(hi, (s + 1) * nu);
       for (int unit = first; unit < end; ++unit) {
-        const int n = (unit - s * nu) * outs + u;
+        const int n = unit * outs + u;
         const bool live = n < p.n_out;
         float w[kHalves];
 #pragma unroll
@@ -513,11 +516,12 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
           // the CTA that brings the last segment's rows of these columns adds them up
           named_barrier(3, kMfEpiThreads);
           if (tid == 0)
-            *last_flag = atom_add_acq_rel_gpu(p.done + (unit - s * nu), 1u) == static_cast<uint32_t>(nseg - 1);
+            *last_flag = atom_add_acq_rel_gpu(p.done + unit, 1u) == static_cast<uint32_t>(nseg - 1);
           named_barrier(3, kMfEpiThreads);
           if (*last_flag) add_up(n - u);
         }
       }
+      k3 = k3 == 2 ? 0 : k3 + 1;
     }
     if (kFuse && p.done != nullptr && nseg == 0) {   // no token has an expert: residual or zero
       pdl_wait_prior_grid();
@@ -539,13 +543,16 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
   const int g = lane >> 2, t4 = lane & 3;
   int slot = 0;
   uint32_t ph = 0;
-  for (int s = s_first, k3 = 0; s * nu < hi; ++s, k3 = k3 == 2 ? 0 : k3 + 1) {
+  bool codes_used = false;
+  for (int s = s_first, k3 = 0; s * width < hi; ++s) {
+    const int first = seg_first(s), end = seg_end(s);
+    if (first >= end) continue;
     const int seg = segs[s];
     const int nt = (mf_seg_count(seg) + 7) >> 3;
-    if (s != s_first) named_barrier(1, kMfConsumers);   // the codes of the segment before are done with
+    if (codes_used) named_barrier(1, kMfConsumers);   // the codes of the segment before are done with
     mf_build_rows<kUp>(p, seg, rows, codes, L.pitch, scales + k3 * 64, scales + 3 * 64, warp, lane);
     named_barrier(1, kMfConsumers);
-    const int first = max(lo, s * nu), end = min(hi, (s + 1) * nu);
+    codes_used = true;
     for (int unit = first; unit < end; ++unit) {
       // two accumulators a tile where few tiles keep the MMAs waiting for one another
       constexpr int kAcc = NT * MT <= 2 ? 2 : 1;
@@ -634,6 +641,7 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
         bph ^= 1u;
       }
     }
+    k3 = k3 == 2 ? 0 : k3 + 1;
   }
 }
 
