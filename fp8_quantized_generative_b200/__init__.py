@@ -335,29 +335,39 @@ def _act(name) -> int:
 
 
 # The FFN operators below serve single tokens, where a call's host time counts:
-# arguments pass through one short test each (what it refuses, _need explains),
+# arguments pass through one plain expression (what it refuses, _refuse explains),
 # the stream handle is read without building a Stream object, and sizes that
 # the library computes are remembered.
 
+_U8, _F16, _F32, _I32 = torch.uint8, torch.float16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _arg(t: torch.Tensor, dtype, ndim: int, dev: int, name: str) -> None:
-    """t must be a contiguous CUDA tensor of this dtype and rank on device number dev."""
-    try:
-        if t.dtype is dtype and t.dim() == ndim and t.get_device() == dev and t.is_contiguous():
-            return
-    except AttributeError:
-        pass
-    _need(t, dtype, name, ndim)
-    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+def _refuse(**args) -> None:
+    """Raise for the first argument that is not a contiguous CUDA tensor of its
+    dtype and rank, or that lies on another device than the first one; name =
+    (tensor, dtype, rank)."""
+    first = None
+    for name, (t, dtype, ndim) in args.items():
+        _need(t, dtype, name, ndim)
+        first = t if first is None else first
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+    raise ValueError("shape mismatch")
 
 
-def _device(t: torch.Tensor, dtype, name: str, ndim: int) -> int:
-    """The device number of the first argument, which the others must share."""
-    _need(t, dtype, name, ndim)
-    return t.get_device()
+def _extra(t: torch.Tensor, dtype, shape: tuple, dev: int, name: str, kind: str) -> int:
+    """Address of an optional argument, which must have this exact shape; 0 for None."""
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, dtype, name, len(shape))
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be {kind}")
 
 
 def linear_epilogue(Xq: torch.Tensor, s_x: torch.Tensor, Wq: torch.Tensor, s_w: torch.Tensor,
@@ -370,36 +380,28 @@ def linear_epilogue(Xq: torch.Tensor, s_x: torch.Tensor, Wq: torch.Tensor, s_w: 
     residual fp16 [M,N], which may be `out` itself."""
     act = _act(activation)
     fmt = _fmt(x_fmt)
-    dev = _device(Xq, torch.uint8, "Xq", 2)
-    _arg(Wq, torch.uint8, 2, dev, "Wq")
-    _arg(s_x, torch.float32, 1, dev, "s_x")
-    _arg(s_w, torch.float32, 1, dev, "s_w")
-    M, K = Xq.shape
-    N, K2 = Wq.shape
-    if K2 != K or s_x.shape[0] != M or s_w.shape[0] != N:
-        raise ValueError("shape mismatch")
-    b = r = 0
-    if bias is not None:
-        _arg(bias, torch.float16, 1, dev, "bias")
-        if bias.shape[0] != N:
-            raise ValueError("bias must be [N]")
-        b = bias.data_ptr()
-    if residual is not None:
-        _arg(residual, torch.float16, 2, dev, "residual")
-        if residual.shape != (M, N):
-            raise ValueError("residual must be [M,N]")
-        r = residual.data_ptr()
-    if out is not None:
-        _arg(out, torch.float16, 2, dev, "out")
-        if out.shape != (M, N):
-            raise ValueError("out must be [M,N]")
+    try:
+        dev = Xq.get_device()
+        (M, K), (N, K2), (M2,), (N2,) = Xq.shape, Wq.shape, s_x.shape, s_w.shape
+        fits = (K2 == K and M2 == M and N2 == N and dev >= 0 and Xq.dtype is _U8 and Wq.dtype is _U8
+                and s_x.dtype is _F32 and s_w.dtype is _F32 and Wq.get_device() == dev and s_x.get_device() == dev
+                and s_w.get_device() == dev and Xq.is_contiguous() and Wq.is_contiguous() and s_x.is_contiguous()
+                and s_w.is_contiguous())
+    except (AttributeError, ValueError):
+        fits = False
+    if not fits:
+        _refuse(Xq=(Xq, _U8, 2), Wq=(Wq, _U8, 2), s_x=(s_x, _F32, 1), s_w=(s_w, _F32, 1))
+    b = _extra(bias, _F16, (N,), dev, "bias", "[N]")
+    r = _extra(residual, _F16, (M, N), dev, "residual", "[M,N]")
+    y = _extra(out, _F16, (M, N), dev, "out", "[M,N]")
     if dev != torch.cuda.current_device():   # the library launches on the current device
         with torch.cuda.device(dev):
             return linear_epilogue(Xq, s_x, Wq, s_w, bias, activation, residual, out, x_fmt)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.float16, device=Xq.device)
+        out = torch.empty(M, N, dtype=_F16, device=Xq.device)
+        y = out.data_ptr()
     check(lib().fp8q_linear_epilogue(Xq.data_ptr(), fmt, s_x.data_ptr(), Wq.data_ptr(), s_w.data_ptr(), M, N, K, b, act,
-                                     r, out.data_ptr(), _raw_stream(dev)), "fp8q_linear_epilogue")
+                                     r, y, _raw_stream(dev)), "fp8q_linear_epilogue")
     return out
 
 
@@ -425,28 +427,27 @@ def moe_route(logits: torch.Tensor, topk: int, renormalize: bool = True) -> MoeR
     rows in the form that quantize_rows_dispatch (token_rows), the grouped
     linears (offsets), the combine (row_token, row_weight) and moe_layer
     (experts, weights) read."""
-    dev = _device(logits, torch.float16, "logits", 2)
+    _need(logits, _F16, "logits", 2)
+    dev = logits.get_device()
     T, E = logits.shape
     if not 1 <= topk <= min(8, E):
         raise ValueError("topk must be in [1, min(8, E)]")
     if dev != torch.cuda.current_device():   # the library launches on the current device
         with torch.cuda.device(dev):
             return moe_route(logits, topk, renormalize)
-    # one allocation for all outputs (each 16-byte aligned) and the workspace
+    # one allocation for all outputs and the workspace
     rows = T * topk
-    pad = (rows + 3) & ~3
-    offs = (E + 4) & ~3
     words = _route_workspace_words(T, E)
-    buf = torch.empty(5 * pad + offs + words, dtype=torch.int32, device=logits.device)
-    base = buf.data_ptr()
-    check(lib().fp8q_moe_route(logits.data_ptr(), T, E, topk, 1 if renormalize else 0, base, base + 12 * pad,
-                               base + 20 * pad, base + 4 * pad, base + 16 * pad, base + 8 * pad,
-                               base + 4 * (5 * pad + offs) if words else 0, _raw_stream(dev)), "fp8q_moe_route")
-    f32 = buf.view(torch.float32)
-    square, line = ((T, topk), (topk, 1)), ((rows,), (1,))
-    return MoeRoute(buf.as_strided(*square, 0), f32.as_strided(*square, 3 * pad),
-                    buf.as_strided((E + 1,), (1,), 5 * pad), buf.as_strided(*line, pad),
-                    f32.as_strided(*line, 4 * pad), buf.as_strided(*square, 2 * pad))
+    i32 = torch.empty(5 * rows + E + 1 + words, dtype=_I32, device=logits.device)
+    base, step = i32.data_ptr(), 4 * rows
+    check(lib().fp8q_moe_route(logits.data_ptr(), T, E, topk, 1 if renormalize else 0, base, base + step,
+                               base + 5 * step, base + 2 * step, base + 3 * step, base + 4 * step,
+                               base + 5 * step + 4 * (E + 1) if words else 0, _raw_stream(dev)), "fp8q_moe_route")
+    f32 = i32.view(_F32)
+    shape, strides = (T, topk), (topk, 1)
+    return MoeRoute(i32.as_strided(shape, strides, 0), f32.as_strided(shape, strides, rows),
+                    i32.as_strided((E + 1,), (1,), 5 * rows), i32.as_strided((rows,), (1,), 2 * rows),
+                    f32.as_strided((rows,), (1,), 3 * rows), i32.as_strided(shape, strides, 4 * rows))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -472,46 +473,43 @@ def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_
     fp16 [T,N] is added (it may be `out` itself).  Larger batches: moe_route and
     the grouped linears."""
     act = _act(activation)
-    dev = _device(X, torch.float16, "X", 2)
-    _arg(experts, torch.int32, 2, dev, "experts")
-    _arg(weights, torch.float32, 2, dev, "weights")
-    _arg(Wq_up, torch.uint8, 3, dev, "Wq_up")
-    _arg(s_up, torch.float32, 2, dev, "s_up")
-    _arg(Wq_down, torch.uint8, 3, dev, "Wq_down")
-    _arg(s_down, torch.float32, 2, dev, "s_down")
-    T, K = X.shape
-    topk = experts.shape[1]
-    E, N, F = Wq_down.shape
-    up_rows = 2 * F if gated else F
-    if (experts.shape[0] != T or weights.shape != experts.shape or Wq_up.shape != (E, up_rows, K)
-            or s_up.shape != (E, up_rows) or s_down.shape != (E, N)):
-        raise ValueError("shape mismatch")
-    r = 0
-    if residual is not None:
-        _arg(residual, torch.float16, 2, dev, "residual")
-        if residual.shape != (T, N):
-            raise ValueError("residual must be [T,N]")
-        r = residual.data_ptr()
-    if out is not None:
-        _arg(out, torch.float16, 2, dev, "out")
-        if out.shape != (T, N):
-            raise ValueError("out must be [T,N]")
+    try:
+        dev = X.get_device()
+        (T, K), (T2, topk), (E, up, K2), (E2, N, F) = X.shape, experts.shape, Wq_up.shape, Wq_down.shape
+        fits = (T2 == T and K2 == K and E2 == E and up == (2 * F if gated else F) and weights.shape == (T, topk)
+                and s_up.shape == (E, up) and s_down.shape == (E, N) and dev >= 0 and X.dtype is _F16
+                and experts.dtype is _I32 and weights.dtype is _F32 and Wq_up.dtype is _U8 and s_up.dtype is _F32
+                and Wq_down.dtype is _U8 and s_down.dtype is _F32 and experts.get_device() == dev
+                and weights.get_device() == dev and Wq_up.get_device() == dev and s_up.get_device() == dev
+                and Wq_down.get_device() == dev and s_down.get_device() == dev and X.is_contiguous()
+                and experts.is_contiguous() and weights.is_contiguous() and Wq_up.is_contiguous()
+                and s_up.is_contiguous() and Wq_down.is_contiguous() and s_down.is_contiguous())
+    except (AttributeError, ValueError):
+        fits = False
+    if not fits:
+        _refuse(X=(X, _F16, 2), experts=(experts, _I32, 2), weights=(weights, _F32, 2), Wq_up=(Wq_up, _U8, 3),
+                s_up=(s_up, _F32, 2), Wq_down=(Wq_down, _U8, 3), s_down=(s_down, _F32, 2))
+    r = _extra(residual, _F16, (T, N), dev, "residual", "[T,N]")
+    y = _extra(out, _F16, (T, N), dev, "out", "[T,N]")
     need = _layer_workspace_bytes(T, topk, F, N)
     if workspace is not None:
-        _arg(workspace, torch.uint8, 1, dev, "workspace")
-        if workspace.shape[0] < need:
+        if workspace.get_device() != dev or workspace.dtype is not _U8 or not workspace.is_contiguous():
+            _refuse(X=(X, _F16, 2), workspace=(workspace, _U8, None))
+        if workspace.numel() < need:
             raise ValueError("workspace does not fit this call")
     if dev != torch.cuda.current_device():   # the library launches on the current device
         with torch.cuda.device(dev):
             return moe_layer(X, experts, weights, Wq_up, s_up, Wq_down, s_down, activation, gated, residual, workspace,
                              out)
+    device = X.device
     if out is None:
-        out = torch.empty(T, N, dtype=torch.float16, device=X.device)
+        out = torch.empty(T, N, dtype=_F16, device=device)
+        y = out.data_ptr()
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = torch.empty(need, dtype=_U8, device=device)
     check(lib().fp8q_moe_layer(X.data_ptr(), T, experts.data_ptr(), weights.data_ptr(), topk, E, Wq_up.data_ptr(),
                                s_up.data_ptr(), Wq_down.data_ptr(), s_down.data_ptr(), K, F, N, act, 1 if gated else 0,
-                               r, out.data_ptr(), workspace.data_ptr(), _raw_stream(dev)), "fp8q_moe_layer")
+                               r, y, workspace.data_ptr(), _raw_stream(dev)), "fp8q_moe_layer")
     return out
 
 

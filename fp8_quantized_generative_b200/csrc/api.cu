@@ -52,6 +52,8 @@ fp8q_status invalid(const char* what) {
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 // ------------------------------------------------------------------ device info
@@ -1171,17 +1173,17 @@ fp8q_status fp8q_moe_route(const void* logits_f16, int64_t T, int32_t E, int32_t
   if (E < 1 || E > kRouteMaxExperts) return invalid("E must be in [1, 1024]");
   if (topk < 1 || topk > kRouteMaxTopk || topk > E) return invalid("topk must be in [1, min(8, E)]");
   if (T < 0 || T > (int64_t(1) << 22)) return invalid("T must be in [0, 2^22]");
-  if (!aligned16(offsets)) return invalid("null or non-16-byte-aligned offsets");
+  if (!aligned4(offsets)) return invalid("null or non-4-byte-aligned offsets");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0) {
     const cudaError_t e = cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (size_t(E) + 1), st);
     if (e != cudaSuccess) return cuda_fail(e, "offsets clear");
     return FP8Q_OK;
   }
-  if (!aligned16(logits_f16) || !aligned16(experts) || !aligned16(weights) || !aligned16(row_token) ||
-      !aligned16(row_weight) || !aligned16(token_rows))
-    return invalid("null or non-16-byte-aligned pointer");
-  if (T > kRouteOneCtaTokens && !aligned16(workspace)) return invalid("null or non-16-byte-aligned workspace");
+  if (logits_f16 == nullptr || (reinterpret_cast<uintptr_t>(logits_f16) & 1u) != 0) return invalid("logits pointer");
+  if (!aligned4(experts) || !aligned4(weights) || !aligned4(row_token) || !aligned4(row_weight) || !aligned4(token_rows))
+    return invalid("null or non-4-byte-aligned pointer");
+  if (T > kRouteOneCtaTokens && !aligned4(workspace)) return invalid("null or non-4-byte-aligned workspace");
   int dev = 0, sms = 0;
   cudaError_t e = current_device_info(&dev, &sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");

@@ -384,6 +384,7 @@ fp8q_status fp8q_linear_epilogue(const uint8_t* Xq, fp8q_format x_fmt, const flo
  * 1024, T <= 2^22; T == 0 writes offsets (zeros) only.  workspace: int32
  * [fp8q_moe_route_workspace_words(T, E)], device, need not be initialized, may be
  * NULL when that is 0; calls whose work overlaps on the GPU need one each.
+ * Pointers are aligned to their element here (4 bytes, logits 2), not to 16.
  */
 fp8q_status fp8q_moe_route(const void* logits_f16, int64_t T, int32_t E, int32_t topk, int renormalize,
                            int32_t* experts, float* weights, int32_t* offsets, int32_t* row_token,

@@ -44,8 +44,8 @@ def route(logits=A, T=4, E=16, topk=2, experts=A, weights=A, offsets=A, row_toke
 
 @pytest.mark.parametrize("bad", [
     dict(E=0), dict(E=1025), dict(topk=0), dict(topk=9), dict(E=4, topk=5), dict(T=-1), dict(T=(1 << 22) + 1),
-    dict(logits=0), dict(logits=BAD), dict(experts=0), dict(weights=BAD), dict(offsets=0), dict(row_token=0),
-    dict(row_weight=0), dict(token_rows=BAD), dict(T=65, ws=0), dict(T=65, ws=BAD),
+    dict(logits=0), dict(logits=A + 1), dict(experts=0), dict(weights=A + 2), dict(offsets=0), dict(offsets=A + 2),
+    dict(row_token=0), dict(row_weight=0), dict(token_rows=A + 2), dict(T=65, ws=0), dict(T=65, ws=A + 2),
 ])
 def test_route_refuses(bad):
     assert route(**bad) == INVALID
@@ -102,3 +102,7 @@ def test_python_wrappers_refuse_cpu_tensors_and_unknown_names():
         fq.moe_layer(torch.zeros((4, 32), dtype=torch.float16), None, None, None, None, None, None)
     with pytest.raises(ValueError, match="activation"):
         fq.moe_layer(None, None, None, None, None, None, None, activation="swish")
+    with pytest.raises(TypeError, match="Xq"):
+        fq.linear_epilogue(None, f32, u8, f32)
+    with pytest.raises(TypeError, match="X must"):
+        fq.moe_layer(None, None, None, None, None, None, None)
