@@ -746,31 +746,42 @@ fp8q_status launch_moe_few(const uint8_t* W, MoeFewParams p, int dev, int sms, c
 // from L2), and at most what leaves the ring two stages.  Weight tiles of a unit: as
 // many as leave a CTA three units or more, so that equal shares differ little
 // (wider units reload the rows less often and leave fewer partial sums).
+struct MoeFewTiles {
+  int nt, mt;
+};
 template <bool kUp, bool kGated>
-fp8q_status launch_moe_few_any(const uint8_t* W, const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
+MoeFewTiles moe_few_tiles(const MoeFewParams& p, int64_t T, int sms) {
   constexpr int kHalves = kUp && kGated ? 2 : 1;
   const int64_t mean2 = (2 * int64_t(p.rows) + p.E - 1) / p.E;
   int64_t rows = mean2 < T ? mean2 : T;
   const MoeFewLayout l = mf_layout(8, 1, p.K, 0, 2, p.rows, p.E);
   const int64_t fit = (kMfMaxSmem - l.total) / l.pitch / 8 * 8;
   if (rows > fit) rows = fit;
-  const int mt = moe_few_share(p, 64 / kHalves, sms) >= 3 ? 4 : moe_few_share(p, 32 / kHalves, sms) >= 3 ? 2 : kHalves;
-  if (rows <= 8) {
-    if (mt == 4) return launch_moe_few<1, 4, kUp, kGated>(W, p, dev, sms, st);
-    if (mt == 2) return launch_moe_few<1, 2, kUp, kGated>(W, p, dev, sms, st);
-    return launch_moe_few<1, kHalves, kUp, kGated>(W, p, dev, sms, st);
+  MoeFewTiles t;
+  t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 || kHalves == 2 ? 4 : 8;
+  t.mt = moe_few_share(p, 64 / kHalves, sms) >= 3 ? 4 : moe_few_share(p, 32 / kHalves, sms) >= 3 ? 2 : kHalves;
+  if (t.nt == 4 && t.mt == 4) t.mt = 2;
+  if (t.nt == 8) t.mt = 1;
+  return t;
+}
+
+template <bool kUp, bool kGated>
+fp8q_status launch_moe_few_any(const uint8_t* W, const MoeFewParams& p, int64_t T, int dev, int sms, cudaStream_t st) {
+  constexpr int kHalves = kUp && kGated ? 2 : 1;
+  const MoeFewTiles t = moe_few_tiles<kUp, kGated>(p, T, sms);
+  switch (t.nt * 10 + t.mt) {
+    case 14: return launch_moe_few<1, 4, kUp, kGated>(W, p, dev, sms, st);
+    case 12: return launch_moe_few<1, 2, kUp, kGated>(W, p, dev, sms, st);
+    case 11: return launch_moe_few<1, kHalves, kUp, kGated>(W, p, dev, sms, st);
+    case 24: return launch_moe_few<2, 4, kUp, kGated>(W, p, dev, sms, st);
+    case 22: return launch_moe_few<2, 2, kUp, kGated>(W, p, dev, sms, st);
+    case 21: return launch_moe_few<2, kHalves, kUp, kGated>(W, p, dev, sms, st);
+    case 42: return launch_moe_few<4, 2, kUp, kGated>(W, p, dev, sms, st);
+    case 41: return launch_moe_few<4, kHalves, kUp, kGated>(W, p, dev, sms, st);
+    default:
+      if constexpr (kHalves == 1) return launch_moe_few<8, 1, kUp, kGated>(W, p, dev, sms, st);
   }
-  if (rows <= 16) {
-    if (mt == 4) return launch_moe_few<2, 4, kUp, kGated>(W, p, dev, sms, st);
-    if (mt == 2) return launch_moe_few<2, 2, kUp, kGated>(W, p, dev, sms, st);
-    return launch_moe_few<2, kHalves, kUp, kGated>(W, p, dev, sms, st);
-  }
-  if (rows <= 32 || kHalves == 2) {
-    if (mt >= 2) return launch_moe_few<4, 2, kUp, kGated>(W, p, dev, sms, st);
-    return launch_moe_few<4, kHalves, kUp, kGated>(W, p, dev, sms, st);
-  }
-  if constexpr (kHalves == 1) return launch_moe_few<8, 1, kUp, kGated>(W, p, dev, sms, st);
-  return FP8Q_ERR_UNSUPPORTED;   // not reached
+  return invalid("fp8q_moe_layer: no such tiles");   // not reached: a gated unit has two weight tiles and four n-tiles at most
 }
 
 }  // namespace
@@ -1259,13 +1270,17 @@ fp8q_status fp8q_moe_layer(const void* X_f16, int64_t T, const int32_t* experts,
   p.act = activation;
   p.hidden = static_cast<__half*>(workspace);
   p.y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + moe_layer_y_offset(rows, F));
-  // Few tokens and at most two units a CTA in the down projection: it adds the rows
-  // up itself, one launch less.  Above, a CTA that comes last brings several units'
-  // sums with it, one after the other, and the separate kernel over all SMs is faster
-  // (measured: 64 tokens 94 us fused, 50 apart; 8 gated tokens 41 against 36).
+  // Few tokens and units a CTA in the down projection: it adds the rows up itself,
+  // one launch less.  Above, a CTA that comes last brings several units' sums with it,
+  // one after the other, and the separate kernel over all SMs is faster (measured: 64
+  // tokens 94 us fused, 50 apart; 8 gated tokens, 6 units, 41 against 36).  In a graph
+  // one token takes 12.3 us fused and 11.6 apart; called from Python, where the host
+  // sets the pace, 15.3 against 17.6.
   MoeFewParams d = p;
+  d.K = static_cast<int>(F);
   d.n_out = static_cast<int>(N);
-  const bool fuse = T <= kMfFuseTokens && moe_few_share(d, 16, sms) <= 2;
+  const MoeFewTiles dt = moe_few_tiles<false, false>(d, T, sms);
+  const bool fuse = T <= kMfFuseTokens && dt.nt <= 2 && moe_few_share(d, 16 * dt.mt, sms) <= kMfFuseUnits;
   if (fuse) {
     p.done = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + moe_layer_done_offset(rows, F, N));
     p.done_units = static_cast<int>((N + 15) / 16);

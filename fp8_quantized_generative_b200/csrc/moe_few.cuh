@@ -59,7 +59,8 @@ constexpr int kMfThreads = kMfConsumers + kMfEpiThreads + 32;   // + the warp th
 constexpr int kMfMaxRows = 1024;       // T * topk
 constexpr int kMfMaxTopk = 8;
 constexpr int kMfMaxExperts = 1024;
-constexpr int kMfFuseTokens = 8;
+constexpr int kMfFuseTokens = 16;      // and units a CTA of the down projection, at most,
+constexpr int kMfFuseUnits = 3;        // for it to add the rows up
 constexpr int kMfStageBytes = 32768;   // RU weight rows x 32 KB / RU of K
 constexpr int kMfMaxStages = 6;
 constexpr int kMfMaxSmem = 232448;     // 227 KB
@@ -76,8 +77,8 @@ struct MoeFewParams {
   int act;                  // up: Activation
   __half* hidden;           // up: [T * topk, F]
   float* y;                 // down: [T * topk, N]
-  // With at most kMfFuseTokens tokens and two units a CTA the down projection also
-  // adds the tokens' rows up (done != nullptr); else moe_few_combine_kernel does.
+  // With few tokens and few units a CTA the down projection also adds the tokens'
+  // rows up (done != nullptr); else moe_few_combine_kernel does.
   uint32_t* done;           // a counter a unit of the down projection, zeroed by the up projection
   int done_units;
   const float* weights;     // [T * topk]
@@ -434,38 +435,42 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
     // (the stores come after the wait below and the partials' first barrier: behind
     // the kernel before this one, as the multiplying warps wait for it)
     const int tid = threadIdx.x - kMfConsumers;
-    // Adding up (one n-tile: at most 8 tokens): this thread's token, four columns of
-    // the unit, and what it needs of the router, loaded ahead.
-    constexpr bool kFuse = !kUp && NT == 1;
+    // Adding up: this thread's first token and four columns of the unit, and what it
+    // needs of the router, loaded ahead.
+    constexpr bool kFuse = !kUp && NT <= 2;   // (more rows than that an expert: never fused)
     constexpr int kVec = outs / 4;
-    static_assert(kMfFuseTokens * kVec <= kMfEpiThreads, "a thread an item");
-    const int ct = tid / kVec, cn = (tid % kVec) * 4;
-    const bool adds = kFuse && p.done != nullptr && ct * p.topk < p.rows;
+    const int tokens = p.rows / p.topk;
     float cw[kMfMaxTopk];
     uint32_t has = 0;   // choices with an expert
-    if (adds) {
+    auto load_choices = [&](int t) {
+      has = 0;
 #pragma unroll
       for (int j = 0; j < kMfMaxTopk; ++j) {
         if (j < p.topk) {
-          const int e = __ldg(p.experts + ct * p.topk + j);
-          cw[j] = __ldg(p.weights + ct * p.topk + j);
+          const int e = __ldg(p.experts + t * p.topk + j);
+          cw[j] = __ldg(p.weights + t * p.topk + j);
           has |= static_cast<uint32_t>(e >= 0 && e < p.E) << j;
         }
       }
-    }
+    };
+    if (kFuse && p.done != nullptr && tid < tokens * kVec) load_choices(tid / kVec);
     auto add_up = [&](int n0) {   // columns n0 .. n0 + outs - 1 of every token
-      const int n = n0 + cn;
-      if (!adds || n >= p.n_out) return;
-      const float* y = p.y + static_cast<int64_t>(ct) * p.topk * p.n_out + n;
-      float4 v[kMfMaxTopk];
+#pragma unroll 1
+      for (int i = tid; i < tokens * kVec; i += kMfEpiThreads) {
+        const int t = i / kVec, n = n0 + (i % kVec) * 4;
+        if (tokens * kVec > kMfEpiThreads) load_choices(t);   // (else every thread keeps its one token)
+        if (n >= p.n_out) continue;
+        const float* y = p.y + static_cast<int64_t>(t) * p.topk * p.n_out + n;
+        float4 v[kMfMaxTopk];
 #pragma unroll
-      for (int j = 0; j < kMfMaxTopk; ++j)
-        if (has >> j & 1u) v[j] = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(j) * p.n_out));
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < kMfMaxTopk; ++j)
+          if (has >> j & 1u) v[j] = __ldcg(reinterpret_cast<const float4*>(y + static_cast<int64_t>(j) * p.n_out));
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < kMfMaxTopk; ++j)
-        if (has >> j & 1u) mf_add_weighted(a, cw[j], v[j]);
-      mf_store_out(p.residual, p.out, static_cast<int64_t>(ct) * p.n_out + n, a);
+        for (int j = 0; j < kMfMaxTopk; ++j)
+          if (has >> j & 1u) mf_add_weighted(a, cw[j], v[j]);
+        mf_store_out(p.residual, p.out, static_cast<int64_t>(t) * p.n_out + n, a);
+      }
     };
     constexpr int step = kMfEpiThreads / outs;
     const int u = tid & (outs - 1), r1 = tid / outs;
