@@ -136,84 +136,110 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
 }
 
 // The same with bias, activation and residual after the scales.  An activation
-// costs more than the sum, so the work is cut finer: an item is one token row x
-// WB weight rows (8, one 16-byte store; 2 where that would leave threads
-// idle), token rows fastest across threads (consecutive words of a partial
-// row).  Bias and residual of a thread's first item are loaded before the
-// mainloop ends (SplitKEpi), the rest when their item comes.  The residual is read by
-// the thread that writes the same outputs, so it may be Y itself.
-template <int WB>
+// costs more than the sum, so the work is cut finer: an item is RB token rows x WB
+// weight rows, as large as leaves no thread idle, token rows
+// fastest across threads (neighbouring words of a partial row).  Bias and residual of
+// a thread's first item are loaded before the mainloop ends, the rest when their item
+// comes.  The residual is read by the thread that writes the same outputs, so it may
+// be Y itself.
+template <int RB, int WB>
 struct SplitKEpi {
   alignas(16) __half b[WB];
-  alignas(16) __half r[WB];
+  alignas(16) __half r[RB][WB];
 };
 
-template <int WB>
-__device__ __forceinline__ void splitk_epi_load(SplitKEpi<WB>& e, const GemmParams& p, int m, int n) {
-  static_assert(WB == 8 || WB == 2, "WB");
-  const int64_t at = static_cast<int64_t>(m) * p.N + n;
-  if constexpr (WB == 8) {
-    if (p.bias != nullptr) *reinterpret_cast<uint4*>(e.b) = __ldg(reinterpret_cast<const uint4*>(p.bias + n));
-    if (p.residual != nullptr) *reinterpret_cast<uint4*>(e.r) = ld_global_v4(p.residual + at);
-  } else {
-    if (p.bias != nullptr) *reinterpret_cast<uint32_t*>(e.b) = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
-    if (p.residual != nullptr) *reinterpret_cast<uint32_t*>(e.r) = ld_global_u32(p.residual + at);
+__device__ __forceinline__ void load_halves(__half (&to)[8], const __half* from) {
+  *reinterpret_cast<uint4*>(to) = ld_global_v4(from);
+}
+__device__ __forceinline__ void load_halves(__half (&to)[2], const __half* from) {
+  *reinterpret_cast<uint32_t*>(to) = ld_global_u32(from);
+}
+
+template <int RB, int WB>
+__device__ __forceinline__ void splitk_epi_load(SplitKEpi<RB, WB>& e, const GemmParams& p, int m, int n) {
+  if (p.bias != nullptr) load_halves(e.b, p.bias + n);
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+      if (m + i < p.rows) load_halves(e.r[i], p.residual + static_cast<int64_t>(m + i) * p.N + n);
   }
 }
 
-// Item idx of an owner's share: token row and first of its weight rows.
-template <int WB>
+// Item idx of an owner's share: first token row and first of its weight rows.
+template <int RB, int WB>
 __device__ __forceinline__ void splitk_epi_item(const GemmParams& p, int idx, int& m, int& nl) {
-  nl = idx / p.rows * WB;
-  m = idx - nl / WB * p.rows;
+  const int groups = (p.rows + RB - 1) / RB;
+  const int w = idx / groups;
+  m = (idx - w * groups) * RB;
+  nl = w * WB;
 }
 
-template <int S, typename L, int WB>
+template <int S, typename L, int RB, int WB>
 __device__ __forceinline__ void splitk_epi_store(const GemmParams& p, const float* send, const float* recv,
                                                  const float* sc_w, const float* sc_x, int n0, int rank, int et,
-                                                 SplitKEpi<WB> e) {
+                                                 SplitKEpi<RB, WB> e) {
   constexpr int SL = kBM / S;
-  const int items = p.rows * (SL / WB);
+  const int items = (p.rows + RB - 1) / RB * (SL / WB);
   for (int idx = et; idx < items; idx += 128) {
     int m, nl;
-    splitk_epi_item<WB>(p, idx, m, nl);
+    splitk_epi_item<RB, WB>(p, idx, m, nl);
     const int n = n0 + rank * SL + nl;
     if (n >= p.N) continue;                        // N % 8 == 0: an item is all in or all out
-    if (idx != et) splitk_epi_load<WB>(e, p, m, n);
-    float z[WB];
+    if (idx != et) splitk_epi_load(e, p, m, n);
+    float z[WB][RB];
 #pragma unroll
-    for (int j = 0; j < WB; ++j) z[j] = 0.0f;
+    for (int j = 0; j < WB; ++j)
+#pragma unroll
+      for (int i = 0; i < RB; ++i) z[j][i] = 0.0f;
 #pragma unroll
     for (int s2 = 0; s2 < S; ++s2) {               // rank order, as the plain linear
       const float* base = (s2 == rank ? send + (rank * SL + nl) * L::kPitch : recv + (s2 * SL + nl) * L::kPitch) + m;
 #pragma unroll
-      for (int j = 0; j < WB; ++j) z[j] = __fadd_rn(z[j], base[j * L::kPitch]);
+      for (int j = 0; j < WB; ++j) {
+        if constexpr (RB == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(base + j * L::kPitch);
+          z[j][0] = __fadd_rn(z[j][0], v.x);
+          z[j][1] = __fadd_rn(z[j][1], v.y);
+          z[j][2] = __fadd_rn(z[j][2], v.z);
+          z[j][3] = __fadd_rn(z[j][3], v.w);
+        } else {
+          z[j][0] = __fadd_rn(z[j][0], base[j * L::kPitch]);
+        }
+      }
     }
-    const float sx = sc_x[m];
-    __half2 h[WB / 2];
 #pragma unroll
-    for (int j = 0; j < WB; ++j) {
-      z[j] = __fmul_rn(__fmul_rn(z[j], sx), sc_w[nl + j]);
-      if (p.bias != nullptr) z[j] = __fadd_rn(z[j], __half2float(e.b[j]));
-      z[j] = activate(z[j], p.act);
-      if (p.residual != nullptr) z[j] = __fadd_rn(z[j], __half2float(e.r[j]));
-      if (j & 1) h[j / 2] = __floats2half2_rn(z[j - 1], z[j]);
+    for (int i = 0; i < RB; ++i) {
+      if (m + i >= p.rows) break;
+      const float sx = sc_x[m + i];
+      alignas(16) __half2 h[WB / 2];
+#pragma unroll
+      for (int j = 0; j < WB; j += 2) {
+        float y[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          y[k] = __fmul_rn(__fmul_rn(z[j + k][i], sx), sc_w[nl + j + k]);
+          if (p.bias != nullptr) y[k] = __fadd_rn(y[k], __half2float(e.b[j + k]));
+          y[k] = activate(y[k], p.act);
+          if (p.residual != nullptr) y[k] = __fadd_rn(y[k], __half2float(e.r[i][j + k]));
+        }
+        h[j / 2] = __floats2half2_rn(y[0], y[1]);
+      }
+      __half* y = p.Y + static_cast<int64_t>(m + i) * p.N + n;
+      if constexpr (WB == 8) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(h);
+      else *reinterpret_cast<__half2*>(y) = h[0];
     }
-    __half* y = p.Y + static_cast<int64_t>(m) * p.N + n;
-    if constexpr (WB == 8) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(h);
-    else *reinterpret_cast<__half2*>(y) = h[0];
   }
 }
 
-template <typename L, int WB>
+template <typename L, int RB, int WB>
 __device__ __forceinline__ void splitk_epi_store_any(const GemmParams& p, const float* send, const float* recv,
                                                      const float* sc_w, const float* sc_x, int n0, int rank, int et,
-                                                     int S, const SplitKEpi<WB>& e) {
+                                                     int S, const SplitKEpi<RB, WB>& e) {
   switch (S) {
-    case 1: splitk_epi_store<1, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
-    case 2: splitk_epi_store<2, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
-    case 4: splitk_epi_store<4, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
-    default: splitk_epi_store<8, L, WB>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    case 1: splitk_epi_store<1, L>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    case 2: splitk_epi_store<2, L>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    case 4: splitk_epi_store<4, L>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
+    default: splitk_epi_store<8, L>(p, send, recv, sc_w, sc_x, n0, rank, et, e); break;
   }
 }
 
@@ -411,17 +437,24 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       if (et < SL) sc_w[et] = n < p.N ? __ldg(p.s_w + n) : 0.0f;
       if (!kFused && et < p.rows) sc_x[et] = __ldg(p.s_x + et);
     }
-    const bool wide = p.rows * SL >= 8 * 128;   // kEpi: items of eight weight rows keep every thread busy
-    SplitKEpi<8> e8;
-    SplitKEpi<2> e2;
+    // kEpi: the largest items that keep every thread busy: 4 x 8 (the loads of the
+    // plain reduction), 1 x 8, 1 x 2.  4096 x 4096 with bias and GELU: 128 rows 10.3 us,
+    // 64 rows 7.9 us (1 x 8 at both: 11.7 and 8.1).
+    const int per_row = p.rows * SL;               // outputs of this owner
+    const int shape = MPAD >= 64 && per_row >= 32 * 128 ? 2 : per_row >= 8 * 128 ? 1 : 0;
+    SplitKEpi<4, 8> e48;
+    SplitKEpi<1, 8> e18;
+    SplitKEpi<1, 2> e12;
     if constexpr (kEpi) {
       int m, nl;
-      if (wide) splitk_epi_item<8>(p, et, m, nl);
-      else splitk_epi_item<2>(p, et, m, nl);
+      if (MPAD >= 64 && shape == 2) splitk_epi_item<4, 8>(p, et, m, nl);
+      else if (shape == 1) splitk_epi_item<1, 8>(p, et, m, nl);
+      else splitk_epi_item<1, 2>(p, et, m, nl);
       const int n = n0 + rank * SL + nl;
       if (nl < SL && n < p.N) {
-        if (wide) splitk_epi_load<8>(e8, p, m, n);
-        else splitk_epi_load<2>(e2, p, m, n);
+        if (MPAD >= 64 && shape == 2) splitk_epi_load(e48, p, m, n);
+        else if (shape == 1) splitk_epi_load(e18, p, m, n);
+        else splitk_epi_load(e12, p, m, n);
       }
     }
     if (kFused) {
@@ -586,8 +619,9 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       raise_error(0x10u);
       *abort_flag = 1;
     } else if constexpr (kEpi) {
-      if (wide) splitk_epi_store_any<L, 8>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e8);
-      else splitk_epi_store_any<L, 2>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e2);
+      if (MPAD >= 64 && shape == 2) splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e48);
+      else if (shape == 1) splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e18);
+      else splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e12);
     } else {
       switch (S) {
         case 1: splitk_reduce_store<1, L>(p, send, recv, sc_w, sc_x, n0, rank, et); break;
