@@ -680,14 +680,58 @@ fp8q_status linear_impl(const uint8_t* Xq, int x_fmt, const float* s_x, const ui
 }
 
 // ------------------------------------------------------------------ router
+// CTAs of the router's cluster: 16 where such a cluster (above the portable size of 8)
+// of this kernel fits on the device, else 8, else 0.
 template <int KPL, int THREADS>
-cudaError_t launch_route(const RouteParams& p, int dev, cudaStream_t st) {
+int route_cluster_size(int dev) {
+  static int cache[kMaxDevices] = {};   // size + 1
+  static std::mutex mu;
+  std::lock_guard<std::mutex> g(mu);
+  if (cache[dev] != 0) return cache[dev] - 1;
+  auto kernel = route_choose_kernel<KPL, THREADS, true>;
+  int size = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    (void)cudaGetLastError();
+  for (int c = kRouteMaxCluster; c >= 8 && size == 0; c /= 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = route_smem(32 * KPL, THREADS / 32);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n >= 1) size = c;
+    else (void)cudaGetLastError();
+  }
+  cache[dev] = size + 1;
+  return size;
+}
+
+template <int KPL, int THREADS>
+cudaError_t launch_route(RouteParams p, int dev, cudaStream_t st) {
   const size_t smem = route_smem(p.E, THREADS / 32), max_smem = route_smem(32 * KPL, THREADS / 32);
-  cudaError_t e = ensure_smem<route_choose_kernel<KPL, THREADS>>(max_smem, dev);
+  cudaError_t e = ensure_smem<route_choose_kernel<KPL, THREADS, true>>(max_smem, dev);
   if (e != cudaSuccess) return e;
-  e = launch_ex(route_choose_kernel<KPL, THREADS>, dim3(p.chunks), dim3(THREADS), smem, st, 1, true, p);
+  if (p.T > kRouteOneCtaTokens && p.T <= kRouteClusterTokens) {
+    const int c = route_cluster_size<KPL, THREADS>(dev);
+    if (c > 0) {
+      p.chunk = (p.T + c - 1) / c;
+      p.chunks = c;
+      return launch_ex(route_choose_kernel<KPL, THREADS, true>, dim3(c), dim3(THREADS), smem, st, c, true, p);
+    }
+  }
+  e = ensure_smem<route_choose_kernel<KPL, THREADS, false>>(max_smem, dev);
+  if (e != cudaSuccess) return e;
+  p.chunk = p.T <= kRouteOneCtaTokens ? p.T : route_chunk(p.T);
+  p.chunks = (p.T + p.chunk - 1) / p.chunk;
+  e = launch_ex(route_choose_kernel<KPL, THREADS, false>, dim3(p.chunks), dim3(THREADS), smem, st, 1, true, p);
   if (e != cudaSuccess || p.chunks == 1) return e;
-  constexpr int kPlaceThreads = 512;
+  constexpr int kPlaceThreads = 1024;
   e = ensure_smem<route_place_kernel<kPlaceThreads>>(route_smem(kRouteMaxExperts, kPlaceThreads / 32), dev);
   if (e != cudaSuccess) return e;
   return launch_ex(route_place_kernel<kPlaceThreads>, dim3(p.chunks), dim3(kPlaceThreads),
@@ -1204,8 +1248,6 @@ fp8q_status fp8q_moe_route(const void* logits_f16, int64_t T, int32_t E, int32_t
   p.E = E;
   p.topk = topk;
   p.renormalize = renormalize != 0;
-  p.chunk = route_chunk(T);
-  p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
   p.experts = experts;
   p.weights = weights;
   p.offsets = offsets;

@@ -17,8 +17,13 @@
 // first rows, and the second walk over the same tokens hands the rows out in
 // order.  No atomic's order reaches a result.
 //
-// Bound: launch and latency at few tokens (one CTA does it all, in one
-// launch); above that two launches, the counts of all chunks in between.
+// Bound: launches and latency.  Up to 64 tokens one CTA; up to 1024 one cluster, whose
+// CTAs read each other's counts from shared memory; both one launch.  Above, two
+// launches over up to 128 CTAs, the counts of all chunks in between: there the choices'
+// instructions want all SMs.  Measured on B200 (graph): 1 token 2.7 us; 256 tokens, 64
+// experts 5.0 us (two launches 6.4); 1000 tokens, 160 experts, 6 choices 10.6 us (8.9,
+// but called from Python, where a launch is what costs, 17.8 against 20.4); 8192
+// tokens, 64 experts 8.5 us (one cluster 22.7).
 #pragma once
 
 #include "ptx.cuh"
@@ -28,6 +33,8 @@ namespace fp8q {
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopk = 8;
 constexpr int kRouteOneCtaTokens = 64;    // at most: one CTA, one launch
+constexpr int kRouteClusterTokens = 1024;  // at most: one cluster
+constexpr int kRouteMaxCluster = 16;
 constexpr int kRouteMaxChunks = 128;      // CTAs of the two-launch form
 
 struct RouteParams {
@@ -45,9 +52,10 @@ struct RouteParams {
   int32_t* counts;        // [chunks, E] workspace of the two-launch form
 };
 
+// Tokens of a CTA of the two-launch form.
 inline int route_chunk(int64_t T) {
   const int64_t c = (T + kRouteMaxChunks - 1) / kRouteMaxChunks;
-  return static_cast<int>(T <= kRouteOneCtaTokens ? (T < 1 ? 1 : T) : c < 32 ? 32 : c);
+  return static_cast<int>(c < 32 ? 32 : c);
 }
 
 // fp16 bits -> 16-bit unsigned of the same order; NaN -> 0, -0 -> +0.
@@ -74,7 +82,7 @@ struct RouteSpan {
 };
 __device__ __forceinline__ RouteSpan route_span(const RouteParams& p, int warp, int warps) {
   const int c0 = static_cast<int>(blockIdx.x) * p.chunk;
-  const int n = min(p.chunk, p.T - c0);
+  const int n = max(0, min(p.chunk, p.T - c0));
   const int per = (n + warps - 1) / warps;
   RouteSpan s;
   s.first = c0 + min(n, warp * per);
@@ -85,14 +93,21 @@ __device__ __forceinline__ RouteSpan route_span(const RouteParams& p, int warp, 
 // Choose the experts of this warp's tokens; count them per expert in `hist`.
 template <int KPL>
 __device__ __forceinline__ void route_choose(const RouteParams& p, const RouteSpan& s, uint16_t* hist, int lane) {
-  for (int t = s.first; t < s.last; ++t) {
+  unsigned short raw[KPL];   // the next token's logits, loaded while one is worked on
+  auto fetch = [&](int t) {
     const unsigned short* src = reinterpret_cast<const unsigned short*>(p.logits + static_cast<int64_t>(t) * p.E);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) raw[i] = lane + 32 * i < p.E ? __ldg(src + lane + 32 * i) : 0;
+  };
+  if (s.first < s.last) fetch(s.first);
+  for (int t = s.first; t < s.last; ++t) {
     uint32_t key[KPL];
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
       const int e = lane + 32 * i;
-      key[i] = e < p.E ? (route_order(__ldg(src + e)) << 16) | (0xffffu - static_cast<uint32_t>(e)) : 0u;
+      key[i] = e < p.E ? (route_order(raw[i]) << 16) | (0xffffu - static_cast<uint32_t>(e)) : 0u;
     }
+    if (t + 1 < s.last) fetch(t + 1);
     float all = 0.0f, m = 0.0f;
     uint32_t mine = 0;   // lane j: the j-th choice
     for (int j = 0; j < p.topk; ++j) {
@@ -129,17 +144,22 @@ __device__ __forceinline__ void route_choose(const RouteParams& p, const RouteSp
   }
 }
 
-// hist[w][e] -> rows of expert e in the warps before w; total[e] -> their sum.
-__device__ __forceinline__ void route_warp_prefix(const RouteParams& p, uint16_t* hist, int* total, int warps) {
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    int acc = 0;
-    for (int w = 0; w < warps; ++w) {
-      const int c = hist[w * p.E + e];
-      hist[w * p.E + e] = static_cast<uint16_t>(acc);
-      acc += c;
+// hist[w][e] -> rows of expert e in the warps before w; returns their sum.
+template <int WARPS>
+__device__ __forceinline__ int route_warp_prefix(uint16_t* hist, int E, int e) {
+  int acc = 0;
+#pragma unroll
+  for (int w0 = 0; w0 < WARPS; w0 += 8) {   // eight reads in flight
+    int c[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) c[u] = hist[(w0 + u) * E + e];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      hist[(w0 + u) * E + e] = static_cast<uint16_t>(acc);
+      acc += c[u];
     }
-    total[e] = acc;
   }
+  return acc;
 }
 
 // Exclusive prefix sum over the experts by one warp: first[e] and, at [E], the sum.
@@ -163,43 +183,62 @@ __device__ __forceinline__ void route_expert_prefix(int E, const int* total, int
   if (lane == 31) first[E] = acc;
 }
 
-// Hand out the rows of this warp's tokens in order.  base[e]: the first row of
-// expert e in this chunk; hist[e]: this warp's next row within it.
-__device__ __forceinline__ void route_place(const RouteParams& p, const RouteSpan& s, uint16_t* hist, const int* base,
-                                            int lane) {
-  for (int t = s.first; t < s.last; ++t) {
-    if (lane < p.topk) {
-      const int64_t at = static_cast<int64_t>(t) * p.topk + lane;
-      const int e = p.experts[at];
-      const float w = p.weights[at];
-      const int row = base[e] + hist[e]++;
-      p.token_rows[at] = row;
-      p.row_token[row] = t;
-      p.row_weight[row] = w;
+// The rows (token, choice) of this warp's tokens, 32 at a time in their order: f(row's
+// position in [T, topk], its expert, its rank among the rows of that expert so far).
+// `hist` counts them per expert.
+template <typename F>
+__device__ __forceinline__ void route_walk(const RouteParams& p, const RouteSpan& s, uint16_t* hist, int lane, F f) {
+  const int64_t last = static_cast<int64_t>(s.last) * p.topk;
+  for (int64_t at0 = static_cast<int64_t>(s.first) * p.topk; at0 < last; at0 += 32) {
+    const int64_t at = at0 + lane;
+    const int e = at < last ? p.experts[at] : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);   // lanes with the same expert
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int before = e >= 0 ? hist[e] : 0;
+    __syncwarp();
+    if (e >= 0) {
+      if (rank == 0) hist[e] = static_cast<uint16_t>(before + __popc(same));
+      f(at, e, before + rank);
     }
     __syncwarp();
   }
 }
 
-// Shared memory: per-warp counters [warps][E] uint16, then two int tables [E + 1].
+// Hand out the rows.  base[e]: the first row of expert e in this chunk; hist[e]: this
+// warp's next row within it.
+__device__ __forceinline__ void route_place(const RouteParams& p, const RouteSpan& s, uint16_t* hist, const int* base,
+                                            int lane) {
+  route_walk(p, s, hist, lane, [&](int64_t at, int e, int place) {
+    const int row = base[e] + place;
+    p.token_rows[at] = row;
+    p.row_token[row] = static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(p.topk));
+    p.row_weight[row] = p.weights[at];
+  });
+}
+
+// Shared memory: per-warp counters [warps][E] uint16, then three int tables [E + 1].
 inline size_t route_smem(int E, int warps) {
-  return ((static_cast<size_t>(warps) * E * 2 + 15) & ~size_t(15)) + 2 * static_cast<size_t>(E + 1) * 4;
+  return ((static_cast<size_t>(warps) * E * 2 + 15) & ~size_t(15)) + 3 * static_cast<size_t>(E + 1) * 4;
 }
 struct RouteTables {
   uint16_t* hist;
   int* total;
   int* first;
+  int* all;
 };
 __device__ __forceinline__ RouteTables route_tables(uint8_t* smem, int E, int warps) {
   RouteTables r;
   r.hist = reinterpret_cast<uint16_t*>(smem);
   r.total = reinterpret_cast<int*>(smem + ((static_cast<size_t>(warps) * E * 2 + 15) & ~size_t(15)));
   r.first = r.total + (E + 1);
+  r.all = r.first + (E + 1);
   return r;
 }
 
-// First launch: choices and counts.  With one chunk it goes on to place the rows.
-template <int KPL, int THREADS>
+// First launch: choices and counts.  One CTA alone goes on to place the rows; so do
+// the CTAs of a cluster (kCluster: the grid is one), each reading the others'
+// counts from their shared memory.
+template <int KPL, int THREADS, bool kCluster>
 __global__ void __launch_bounds__(THREADS) route_choose_kernel(const RouteParams p) {
   extern __shared__ __align__(16) uint8_t route_smem_raw[];
   constexpr int kWarps = THREADS / 32;
@@ -213,8 +252,40 @@ __global__ void __launch_bounds__(THREADS) route_choose_kernel(const RouteParams
   uint16_t* hist = tb.hist + warp * p.E;
   route_choose<KPL>(p, s, hist, lane);
   __syncthreads();
-  route_warp_prefix(p, tb.hist, tb.total, kWarps);
+  for (int e = threadIdx.x; e < p.E; e += THREADS) tb.total[e] = route_warp_prefix<kWarps>(tb.hist, p.E, e);
   __syncthreads();
+  if (kCluster) {
+    cluster_arrive();
+    cluster_wait();
+    const int rank = static_cast<int>(cluster_ctarank()), n = static_cast<int>(cluster_nctarank());
+    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+      const uint32_t at = smem_u32(tb.total + e);
+      int before = 0, sum = 0;
+      for (int c0 = 0; c0 < n; c0 += 8) {   // (n is 8 or 16)
+        int v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = ld_dsmem_i32(mapa_shared(at, static_cast<uint32_t>(c0 + u)));
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          sum += v[u];
+          if (c0 + u < rank) before += v[u];
+        }
+      }
+      tb.all[e] = sum;
+      tb.first[e] = before;
+    }
+    __syncthreads();
+    cluster_arrive();   // no CTA leaves while another reads its counts
+    if (warp == 0) route_expert_prefix(p.E, tb.all, tb.all, lane);   // all[e] -> first row of expert e
+    __syncthreads();
+    if (rank == 0)
+      for (int e = threadIdx.x; e <= p.E; e += THREADS) p.offsets[e] = tb.all[e];
+    for (int e = threadIdx.x; e < p.E; e += THREADS) tb.first[e] += tb.all[e];
+    __syncthreads();
+    route_place(p, s, hist, tb.first, lane);
+    cluster_wait();
+    return;
+  }
   if (p.chunks > 1) {
     for (int e = threadIdx.x; e < p.E; e += THREADS)
       p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = tb.total[e];
@@ -244,10 +315,16 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
   for (int i = threadIdx.x; i < parts * p.E; i += THREADS) {
     const int e = i % p.E;
     int before = 0, sum = 0;
-    for (int c = i / p.E; c < p.chunks; c += parts) {
-      const int v = p.counts[static_cast<int64_t>(c) * p.E + e];
-      sum += v;
-      if (c < static_cast<int>(blockIdx.x)) before += v;
+    for (int c0 = i / p.E; c0 < p.chunks; c0 += 8 * parts) {   // eight loads in flight
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = c0 + u * parts < p.chunks ? p.counts[static_cast<int64_t>(c0 + u * parts) * p.E + e] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        sum += v[u];
+        if (c0 + u * parts < static_cast<int>(blockIdx.x)) before += v[u];
+      }
     }
     atomicAdd(&tb.total[e], sum);      // integers: the order does not matter
     atomicAdd(&tb.first[e], before);
@@ -255,10 +332,7 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
   // this warp's rows per expert
   const RouteSpan s = route_span(p, warp, kWarps);
   uint16_t* hist = tb.hist + warp * p.E;
-  for (int t = s.first; t < s.last; ++t) {
-    if (lane < p.topk) ++hist[p.experts[static_cast<int64_t>(t) * p.topk + lane]];
-    __syncwarp();
-  }
+  route_walk(p, s, hist, lane, [](int64_t, int, int) {});
   __syncthreads();
   if (warp == 0) route_expert_prefix(p.E, tb.total, tb.total, lane);   // total[e] -> first row of expert e
   __syncthreads();
@@ -266,12 +340,7 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
     for (int e = threadIdx.x; e <= p.E; e += THREADS) p.offsets[e] = tb.total[e];
   for (int e = threadIdx.x; e < p.E; e += THREADS) {
     tb.first[e] += tb.total[e];
-    int acc = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = tb.hist[w * p.E + e];
-      tb.hist[w * p.E + e] = static_cast<uint16_t>(acc);
-      acc += c;
-    }
+    route_warp_prefix<kWarps>(tb.hist, p.E, e);
   }
   __syncthreads();
   route_place(p, s, hist, tb.first, lane);
