@@ -357,7 +357,8 @@ typedef enum {
  * fp16, either may be NULL (left out); without both and with FP8Q_ACT_NONE
  * the result is fp8q_linear_fmt's bit for bit.  residual_f16 may be Y_f16
  * itself (added in place), and may not overlap it otherwise.  Kernel choice as
- * for fp8q_linear; of fp8q_set_gemm_tuning, tile_n = 512 is taken as 256.
+ * for fp8q_linear; of fp8q_set_gemm_tuning, tile_n = 512 is taken as 256, and
+ * the stage-size environment variables (see there) do not apply.
  */
 fp8q_status fp8q_linear_epilogue(const uint8_t* Xq, fp8q_format x_fmt, const float* s_x,
                                  const uint8_t* Wq, const float* s_w,
