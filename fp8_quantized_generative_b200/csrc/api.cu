@@ -804,6 +804,9 @@ MoeFewTiles moe_few_tiles(const MoeFewParams& p, int64_t T, int sms) {
   MoeFewTiles t;
   t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 || kHalves == 2 ? 4 : 8;
   t.mt = moe_few_share(p, 64 / kHalves, sms) >= 3 ? 4 : moe_few_share(p, 32 / kHalves, sms) >= 3 ? 2 : kHalves;
+  // Where the longest rows leave no room beside the partial sums counted above, half
+  // as many partial sums: then any K up to 8192 fits.
+  if (fit < 8 && t.mt == 4) t.mt = 2;
   if (t.nt == 4 && t.mt == 4) t.mt = 2;
   if (t.nt == 8) t.mt = 1;
   return t;

@@ -89,6 +89,15 @@ def test_long_rows(fq, K, F):
         check(fq, T, 4, 2, K, F, 136, seed=T)
 
 
+@pytest.mark.parametrize("T,E,K,F,N,gated", [
+    (128, 8, 8192, 2432, 8, False), (128, 8, 8192, 1216, 8, True), (128, 8, 16, 8192, 2432, False),
+    (32, 64, 8176, 272, 16, False),
+])
+def test_longest_rows_with_many_units(fq, T, E, K, F, N, gated):
+    """The longest rows beside the row lists of many choices, and enough units for wide ones."""
+    check(fq, T, E, 8, K, F, N, gated=gated, seed=T + F)
+
+
 @pytest.mark.parametrize("T", [9, 64, 128])
 def test_all_tokens_to_one_expert(fq, T):
     """More rows than one segment holds."""
