@@ -8,8 +8,10 @@
 //   silu       z / (1 + e^-z)
 //   gelu_tanh  0.5 z (1 + tanh u) = z / (1 + e^-2u),  u = sqrt(2/pi) (z + 0.044715 z^3)
 //              Both: one exponential a value and one reciprocal for two, 1/a = b / (ab).
-//              The exponent of 2 is cut at 60, which keeps the product finite; past it
-//              the result is under 2^-43.
+//              The exponent of 2 is cut at 60, which keeps the product finite (at 126 where
+//              a value has its own reciprocal), and the factor z at -128, where the
+//              exponent has long been cut: the result there is under 2^-53, however
+//              negative z is.
 //   gelu       z Phi(z) = max(z, 0) - u Phi(-u) with u = |z|, Phi the normal
 //              distribution function, whose log2 Phi(-u) is smooth: a polynomial of
 //              degree 7, a least-squares fit over 0 <= u <= 6 reweighted towards the
@@ -17,8 +19,8 @@
 //              fp32, the far negative tail included) with one exponential.  u is cut at
 //              6: u Phi(-u) is below 6e-9 from there on, under half of fp16's least step.
 // The pair forms do the multiply-adds of two values in one instruction
-// (f32x2, the same roundings).  4096 x 8192 x 256, where the epilogue is all the time:
-// GELU 44.6 us with a division and an exponential a value, SILU 40.6.
+// (f32x2, the same roundings).  4096 x 8192 x 256 with bias, where the epilogue is all
+// the time: none 32 us, SILU 39, GELU 42, GELU_TANH 40.
 // NaN stays NaN.
 #pragma once
 
@@ -76,7 +78,9 @@ constexpr float kLog2e = 1.44269504088896f;
 // -2 u log2(e) = z (kTanh0 + kTanh1 z^2)
 constexpr float kTanh0 = -1.59576912160573f * kLog2e;    // -2 sqrt(2/pi) log2(e)
 constexpr float kTanh1 = -0.0713548162726009f * kLog2e;  // the same times 0.044715
-constexpr float kGateCut = 60.0f;
+constexpr float kGateCut = 60.0f;     // two values to a reciprocal
+constexpr float kGateCutOne = 126.0f;
+constexpr float kGateFloor = -128.0f;
 constexpr float kGeluCut = 6.0f;
 // log2 Phi(-u) = kGelu0 + u (kGelu1 + ..)
 constexpr float kGelu0 = -0.999995294f, kGelu1 = -1.15125105f, kGelu2 = -0.458464391f, kGelu3 = -0.0539600711f,
@@ -85,6 +89,8 @@ constexpr float kGelu0 = -0.999995294f, kGelu1 = -1.15125105f, kGelu2 = -0.45846
 // z / (1 + 2^e2)
 __device__ __forceinline__ F32x2 gate2(F32x2 z, F32x2 e2) {
   float a, b;
+  unpack2(z, a, b);
+  z = pack2(max_nan(a, kGateFloor), max_nan(b, kGateFloor));
   unpack2(e2, a, b);
   unpack2(add2(pack2(ex2_approx(fminf(a, kGateCut)), ex2_approx(fminf(b, kGateCut))), both(1.0f)), a, b);
   return mul2(z, mul2(both(rcp_approx(__fmul_rn(a, b))), pack2(b, a)));
@@ -128,10 +134,10 @@ __device__ __forceinline__ float activate(float z, int act) {
     q = fmaf(q, u, kGelu3);
     q = fmaf(q, u, kGelu2);
     q = fmaf(q, u, kGelu1);
-    return fmaf(-u, ex2_approx(fmaf(q, u, kGelu0)), r);
+    return u < kGeluCut ? fmaf(-u, ex2_approx(fmaf(q, u, kGelu0)), r) : r;   // (a gate may multiply what the cut leaves)
   }
   const float e = act == kActSilu ? __fmul_rn(z, -kLog2e) : __fmul_rn(z, fmaf(__fmul_rn(z, z), kTanh1, kTanh0));
-  return __fmul_rn(z, rcp_approx(__fadd_rn(ex2_approx(fminf(e, kGateCut)), 1.0f)));
+  return __fmul_rn(max_nan(z, kGateFloor), rcp_approx(__fadd_rn(ex2_approx(fminf(e, kGateCutOne)), 1.0f)));
 }
 
 }  // namespace fp8q

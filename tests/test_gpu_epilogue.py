@@ -150,3 +150,24 @@ def test_ffn_pair_full(fq):
         terms = terms + np.abs(to_np(bias).astype(np.float64))[None, :]
         assert_within(to_np(Y)[rows], y, linear_epilogue_bound(K, y, terms, rr), f"{M}x{N}x{K}")
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("M", [2, 100, 200])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_activations_of_large_values(fq, act, M):
+    """Products +-2^j up to 2^124: the activation is z (rounded to fp16) or, exactly, zero.
+    From |z| = 128 on that is every formula's fp16 value: z's own tail, z e^z, is below 2^-170."""
+    K, powers = 16, np.arange(3, 121)
+    N = 240
+    one = torch.tensor([1.0]).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    Xq = torch.full((M, K), one, dtype=torch.uint8, device="cuda")
+    Wq = torch.full((N, K), one, dtype=torch.uint8, device="cuda")
+    Wq[1::2] |= 0x80
+    j = np.resize(np.repeat(powers, 2), N)
+    s_w = torch.from_numpy(np.exp2(j).astype(np.float32)).cuda()
+    out = fq.linear_epilogue(Xq, torch.ones(M, device="cuda"), Wq, s_w, activation=act)
+    got = to_np(out).astype(np.float64)
+    with np.errstate(over="ignore"):
+        want = np.where(np.arange(N) % 2 == 0, (K * np.exp2(j)).astype(np.float16), 0).astype(np.float64)
+    assert np.array_equal(got, np.broadcast_to(want, got.shape))
+    assert_no_device_error()

@@ -125,6 +125,27 @@ def test_no_token_has_an_expert(fq):
     check(fq, 4, 7, 2, 144, 96, 80, experts=np.full((4, 2), -1))
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_large_negative_products(fq, act, gated):
+    """Up projections from -2^9 to -2^84: hidden rows of zeros, whatever multiplies them."""
+    T, K, F, N = 3, 64, 16, 16
+    X = torch.full((T, K), 1.0, dtype=torch.float16, device="cuda")
+    Wu, su = fq.quantize_weight_per_channel(torch.full((1, 2 * F if gated else F, K), 0.125, dtype=torch.float16,
+                                                       device="cuda"))
+    Wu[:, :F] |= 0x80
+    su = su * torch.exp2(torch.arange(F, device="cuda") * 5.0 + 6.0).repeat(2 if gated else 1)
+    if gated:
+        su[:, F:] = 0.125 / 448
+    Wd, sd = fq.quantize_weight_per_channel(wl.random_f16((1, N, F), seed=1).cuda())
+    ws = fq.moe_layer_workspace(T, 1, F, N, "cuda")
+    out = fq.moe_layer(X, torch.zeros((T, 1), dtype=torch.int32, device="cuda"), torch.ones((T, 1), device="cuda"),
+                       Wu, su, Wd, sd, activation=act, gated=gated, workspace=ws)
+    assert bool((ws[:T * F * 2].view(torch.float16) == 0).all())
+    assert bool((out == 0).all())
+    assert_no_device_error()
+
+
 def test_residual_in_place(fq):
     check(fq, 10, 8, 2, 272, 144, 136, in_place=True)
 
