@@ -493,7 +493,8 @@ def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_
     y = _extra(out, _F16, (T, N), dev, "out", "[T,N]")
     need = _layer_workspace_bytes(T, topk, F, N)
     if workspace is not None:
-        if workspace.get_device() != dev or workspace.dtype is not _U8 or not workspace.is_contiguous():
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or workspace.dtype is not _U8 \
+                or not workspace.is_contiguous():
             _refuse(X=(X, _F16, 2), workspace=(workspace, _U8, None))
         if workspace.numel() < need:
             raise ValueError("workspace does not fit this call")

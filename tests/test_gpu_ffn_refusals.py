@@ -58,6 +58,11 @@ def test_wrong_tensors(fq, op):
     assert fq.device_error() == 0
 
 
+def test_workspace_that_is_no_tensor(fq):
+    with pytest.raises(TypeError, match="workspace"):
+        fq.moe_layer(**{**layer_args(), "workspace": "not a tensor"})
+
+
 def test_small_workspace_and_missing_arguments(fq):
     args = layer_args()
     args["workspace"] = t(u8, 16)
