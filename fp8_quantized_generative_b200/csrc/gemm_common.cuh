@@ -244,13 +244,14 @@ __device__ __forceinline__ void epilogue_residual(uint4 (&r)[4], const GemmParam
   }
 }
 
-template <int ACT>
-__device__ __forceinline__ void activate_pairs(F32x2 (&z)[8]) {
+template <int ACT, int P>
+__device__ __forceinline__ void activate_pairs(F32x2 (&z)[P]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = activate2<ACT>(z[i]);
+  for (int i = 0; i < P; ++i) z[i] = activate2<ACT>(z[i]);
 }
 
-__device__ __forceinline__ void activate_pairs_any(F32x2 (&z)[8], int act) {
+template <int P>
+__device__ __forceinline__ void activate_pairs_any(F32x2 (&z)[P], int act) {
   switch (act) {   // uniform
     case kActRelu: activate_pairs<kActRelu>(z); break;
     case kActGelu: activate_pairs<kActGelu>(z); break;

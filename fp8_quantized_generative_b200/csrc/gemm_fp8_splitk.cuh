@@ -207,22 +207,35 @@ __device__ __forceinline__ void splitk_epi_store(const GemmParams& p, const floa
         }
       }
     }
+    constexpr int WP = WB / 2;
+    F32x2 y2[RB * WP];                             // pairs of weight rows (sc_x has MPAD rows: any m + i is in it)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const F32x2 sx = both(sc_x[m + i]);
+#pragma unroll
+      for (int j = 0; j < WP; ++j)
+        y2[i * WP + j] = mul2(mul2(pack2(z[2 * j][i], z[2 * j + 1][i]), sx), pack2(sc_w[nl + 2 * j], sc_w[nl + 2 * j + 1]));
+    }
+    if (p.bias != nullptr) {
+#pragma unroll
+      for (int j = 0; j < WP; ++j) {
+        const F32x2 b = pack2(__half2float(e.b[2 * j]), __half2float(e.b[2 * j + 1]));
+#pragma unroll
+        for (int i = 0; i < RB; ++i) y2[i * WP + j] = add2(y2[i * WP + j], b);
+      }
+    }
+    activate_pairs_any(y2, p.act);
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
       if (m + i >= p.rows) break;
-      const float sx = sc_x[m + i];
-      alignas(16) __half2 h[WB / 2];
+      alignas(16) __half2 h[WP];
 #pragma unroll
-      for (int j = 0; j < WB; j += 2) {
-        float y[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          y[k] = __fmul_rn(__fmul_rn(z[j + k][i], sx), sc_w[nl + j + k]);
-          if (p.bias != nullptr) y[k] = __fadd_rn(y[k], __half2float(e.b[j + k]));
-          y[k] = activate(y[k], p.act);
-          if (p.residual != nullptr) y[k] = __fadd_rn(y[k], __half2float(e.r[i][j + k]));
-        }
-        h[j / 2] = __floats2half2_rn(y[0], y[1]);
+      for (int j = 0; j < WP; ++j) {
+        if (p.residual != nullptr)
+          y2[i * WP + j] = add2(y2[i * WP + j], pack2(__half2float(e.r[i][2 * j]), __half2float(e.r[i][2 * j + 1])));
+        float lo, hi;
+        unpack2(y2[i * WP + j], lo, hi);
+        h[j] = __floats2half2_rn(lo, hi);
       }
       __half* y = p.Y + static_cast<int64_t>(m + i) * p.N + n;
       if constexpr (WB == 8) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(h);
