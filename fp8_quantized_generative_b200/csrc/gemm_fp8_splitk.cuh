@@ -135,9 +135,11 @@ __device__ __forceinline__ void splitk_reduce_store(const GemmParams& p, const f
   }
 }
 
-// The same with bias, activation and residual after the scales.  An activation
-// costs more than the sum, so the work is cut finer: an item is RB token rows x WB
-// weight rows, as large as leaves no thread idle, token rows
+// The same with bias, activation and residual after the scales.  This code runs once
+// or twice a launch, so what bounds it is fetching its instructions: an item's values
+// go through the activation in pairs under one branch (a branch per value: 128 rows of
+// 4096 x 4096 with bias and GELU 11.2 us against 9.4), and a kernel holds as few item
+// shapes as it can.  An item is RB token rows x WB weight rows, token rows
 // fastest across threads (neighbouring words of a partial row).  Bias and residual of
 // a thread's first item are loaded before the mainloop ends, the rest when their item
 // comes.  The residual is read by the thread that writes the same outputs, so it may
@@ -450,22 +452,23 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       if (et < SL) sc_w[et] = n < p.N ? __ldg(p.s_w + n) : 0.0f;
       if (!kFused && et < p.rows) sc_x[et] = __ldg(p.s_x + et);
     }
-    // kEpi: the largest items that keep every thread busy: 4 x 8 (the loads of the
-    // plain reduction), 1 x 8, 1 x 2.  4096 x 4096 with bias and GELU: 128 rows 10.3 us,
-    // 64 rows 7.9 us (1 x 8 at both: 11.7 and 8.1).
-    const int per_row = p.rows * SL;               // outputs of this owner
-    const int shape = MPAD >= 64 && per_row >= 32 * 128 ? 2 : per_row >= 8 * 128 ? 1 : 0;
+    // kEpi: the item shape, 2: 4 x 8 (the loads of the plain reduction), 1: 1 x 8, 0: 1 x 2.
+    // Bias and GELU, us: 64 rows of 4096 x 4096 7.0 with 4 x 8 alone, 7.4 with 1 x 8 beside
+    // it for shares that leave threads idle (100 rows of 1000 x 1040: 6.4 and 7.2); 32 rows
+    // 5.6 with 1 x 8, 6.1 with 4 x 8.  Up to 16 rows 1 x 2 where that is one item a thread:
+    // 4 rows 5.1, with 1 x 8 5.3; past that 1 x 8: 16 rows 5.3, with 1 x 2 5.6.
+    const int shape = MPAD >= 64 ? 2 : MPAD == 32 || p.rows * SL > 2 * 128 ? 1 : 0;
     SplitKEpi<4, 8> e48;
     SplitKEpi<1, 8> e18;
     SplitKEpi<1, 2> e12;
     if constexpr (kEpi) {
       int m, nl;
-      if (MPAD >= 64 && shape == 2) splitk_epi_item<4, 8>(p, et, m, nl);
+      if (shape == 2) splitk_epi_item<4, 8>(p, et, m, nl);
       else if (shape == 1) splitk_epi_item<1, 8>(p, et, m, nl);
       else splitk_epi_item<1, 2>(p, et, m, nl);
       const int n = n0 + rank * SL + nl;
       if (nl < SL && n < p.N) {
-        if (MPAD >= 64 && shape == 2) splitk_epi_load(e48, p, m, n);
+        if (shape == 2) splitk_epi_load(e48, p, m, n);
         else if (shape == 1) splitk_epi_load(e18, p, m, n);
         else splitk_epi_load(e12, p, m, n);
       }
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(kSkThreads, 1)
       raise_error(0x10u);
       *abort_flag = 1;
     } else if constexpr (kEpi) {
-      if (MPAD >= 64 && shape == 2) splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e48);
+      if (shape == 2) splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e48);
       else if (shape == 1) splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e18);
       else splitk_epi_store_any<L>(p, send, recv, sc_w, sc_x, n0, rank, et, S, e12);
     } else {
