@@ -235,11 +235,14 @@ __device__ __forceinline__ uint2 quantize4_f16(const uint2& v, float r) {
 
 // Quantize the rows of a segment into shared memory (the fp16 values of the codes
 // [cnt][pitch], zero behind K, pairs permuted as above; scales).  A lane first
-// copies its 16-byte pieces of the row to where their codes will lie, eight loads in
+// copies its 16-byte pieces of the row to where their codes will lie, kLoads loads in
 // flight, with the maximum on the way, and then converts them in place: one read
 // from global for any K, in little code (the kernel starts cold).  With few rows
-// several warps share one; their maxima meet in `maxima`.
-template <bool kUp>
+// several warps share one; their maxima meet in `maxima`.  kLoads: eight where a CTA
+// has many units and starts segments while its weights stream, four where the start is
+// most of the time (one token of 64 experts, 2048-1024-2048, 12.8 -> 12.2 us for the
+// layer; 64 tokens with four 49.3 -> 53.0).
+template <bool kUp, int kLoads>
 __device__ __forceinline__ void mf_build_rows(const MoeFewParams& p, int seg, const int* rows, uint8_t* codes,
                                               int pitch, float* scales, float* maxima, int warp, int lane) {
   const int cnt = mf_seg_count(seg), row0 = mf_seg_row0(seg);
@@ -258,13 +261,13 @@ __device__ __forceinline__ void mf_build_rows(const MoeFewParams& p, int seg, co
       const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(kUp ? slot / p.topk : slot) * p.K);
       __half2 m2 = __float2half2_rn(0.0f);
 #pragma unroll 1
-      for (int j = j0; j < nvec_pad; j += 8 * step) {
-        uint4 v[8];
+      for (int j = j0; j < nvec_pad; j += kLoads * step) {
+        uint4 v[kLoads];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kLoads; ++u)
           v[u] = j + u * step < nvec ? ld_global_v4(src + j + u * step) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kLoads; ++u) {
           m2 = absmax8_f16(v[u], m2);
           if (j + u * step < nvec_pad) {
             uint8_t* at = dst + (j - j0 + u * step) * 16;
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kMfThreads) moe_few_kernel(const __grid_consta
     const int seg = segs[s];
     const int nt = (mf_seg_count(seg) + 7) >> 3;
     if (codes_used) named_barrier(1, kMfConsumers);   // the codes of the segment before are done with
-    mf_build_rows<kUp>(p, seg, rows, codes, L.pitch, scales + k3 * 64, scales + 3 * 64, warp, lane);
+    mf_build_rows<kUp, MT == 4 ? 8 : 4>(p, seg, rows, codes, L.pitch, scales + k3 * 64, scales + 3 * 64, warp, lane);
     named_barrier(1, kMfConsumers);
     codes_used = true;
     for (int unit = first; unit < end; ++unit) {
