@@ -16,8 +16,12 @@
 //              distribution function, whose log2 Phi(-u) is smooth: a polynomial of
 //              degree 7, a least-squares fit over 0 <= u <= 6 reweighted towards the
 //              largest error, gives Phi(-u) to a relative 3.3e-6 (6.6e-6 evaluated in
-//              fp32, the far negative tail included) with one exponential.  u is cut at
-//              6: u Phi(-u) is below 6e-9 from there on, under half of fp16's least step.
+//              fp32) with one exponential.  The pair form cuts u at 6: u Phi(-u) is below
+//              6e-9 from there on, under half of fp16's least step, and nothing multiplies it.
+//              The form for one value, which a gate may multiply by anything, goes on with
+//              u Phi(-u) = phi(u) Q(1 / u^2) from 6 on, phi the normal density and Q a
+//              least-squares fit of degree 3 (relative 1.1e-7; 8e-6 evaluated in fp32, where
+//              the roundings of the exponent, up to 126, are most of it) down to 2^-126.
 // The pair forms do the multiply-adds of two values in one instruction
 // (f32x2, the same roundings).  4096 x 8192 x 256 with bias, where the epilogue is all
 // the time: none 32 us, SILU 39, GELU 42, GELU_TANH 40.
@@ -85,6 +89,9 @@ constexpr float kGeluCut = 6.0f;
 // log2 Phi(-u) = kGelu0 + u (kGelu1 + ..)
 constexpr float kGelu0 = -0.999995294f, kGelu1 = -1.15125105f, kGelu2 = -0.458464391f, kGelu3 = -0.0539600711f,
                 kGelu4 = 0.00850789188f, kGelu5 = -0.000930525087f, kGelu6 = 6.15983236e-05f, kGelu7 = -1.83481289e-06f;
+// log2 phi(u) = kPhi0 + kPhi1 u^2,  Q(w) = kTail0 + w (kTail1 + ..)
+constexpr float kPhi0 = -1.32574806f, kPhi1 = -0.5f * kLog2e;
+constexpr float kTail0 = 0.999997139f, kTail1 = -0.999070108f, kTail2 = 2.89569616f, kTail3 = -9.96920872f;
 
 // z / (1 + 2^e2)
 __device__ __forceinline__ F32x2 gate2(F32x2 z, F32x2 e2) {
@@ -127,14 +134,22 @@ __device__ __forceinline__ float activate(float z, int act) {
   const float r = max_nan(z, 0.0f);
   if (act == kActRelu) return r;
   if (act == kActGelu) {
-    const float u = fminf(fabsf(z), kGeluCut);
-    float q = fmaf(u, kGelu7, kGelu6);
-    q = fmaf(q, u, kGelu5);
-    q = fmaf(q, u, kGelu4);
-    q = fmaf(q, u, kGelu3);
-    q = fmaf(q, u, kGelu2);
-    q = fmaf(q, u, kGelu1);
-    return u < kGeluCut ? fmaf(-u, ex2_approx(fmaf(q, u, kGelu0)), r) : r;   // (a gate may multiply what the cut leaves)
+    const float u = fabsf(z);
+    float f = u, q;   // u Phi(-u) = f 2^q
+    if (u < kGeluCut) {
+      q = fmaf(u, kGelu7, kGelu6);
+      q = fmaf(q, u, kGelu5);
+      q = fmaf(q, u, kGelu4);
+      q = fmaf(q, u, kGelu3);
+      q = fmaf(q, u, kGelu2);
+      q = fmaf(q, u, kGelu1);
+      q = fmaf(q, u, kGelu0);
+    } else {
+      const float t = __fmul_rn(u, u), w = rcp_approx(t);
+      f = fmaf(fmaf(fmaf(kTail3, w, kTail2), w, kTail1), w, kTail0);
+      q = fmaf(t, kPhi1, kPhi0);
+    }
+    return fmaf(-f, ex2_approx(q), r);
   }
   const float e = act == kActSilu ? __fmul_rn(z, -kLog2e) : __fmul_rn(z, fmaf(__fmul_rn(z, z), kTanh1, kTanh0));
   return __fmul_rn(max_nan(z, kGateFloor), rcp_approx(__fadd_rn(ex2_approx(fminf(e, kGateCutOne)), 1.0f)));
