@@ -24,7 +24,6 @@ FP8Q_FMT_E5M2 = 1
 FORMATS = {"e4m3": FP8Q_FMT_E4M3, "e5m2": FP8Q_FMT_E5M2}
 
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # FP8Q_ACT_*
-MOE_LAYER_MAX_TOKENS = 128
 
 DEVERR_TIMEOUT_PRODUCER = 0x1
 DEVERR_TIMEOUT_MMA = 0x2

@@ -739,6 +739,7 @@ cudaError_t launch_route(RouteParams p, int dev, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ MoE layer for a few tokens
+static_assert(FP8Q_MOE_LAYER_MAX_TOKENS * kMfMaxTopk <= kMfMaxRows, "rows of the largest layer");
 // Workspace: hidden rows fp16 [rows, F], y fp32 [rows, N], a counter per unit of the
 // down projection (units of 16 outputs at least).
 int64_t moe_layer_y_offset(int64_t rows, int64_t F) { return (rows * F * 2 + 255) & ~int64_t(255); }
@@ -819,16 +820,19 @@ fp8q_status launch_moe_few_any(const uint8_t* W, const MoeFewParams& p, int64_t 
   switch (t.nt * 10 + t.mt) {
     case 14: return launch_moe_few<1, 4, kUp, kGated>(W, p, dev, sms, st);
     case 12: return launch_moe_few<1, 2, kUp, kGated>(W, p, dev, sms, st);
-    case 11: return launch_moe_few<1, kHalves, kUp, kGated>(W, p, dev, sms, st);
     case 24: return launch_moe_few<2, 4, kUp, kGated>(W, p, dev, sms, st);
     case 22: return launch_moe_few<2, 2, kUp, kGated>(W, p, dev, sms, st);
-    case 21: return launch_moe_few<2, kHalves, kUp, kGated>(W, p, dev, sms, st);
     case 42: return launch_moe_few<4, 2, kUp, kGated>(W, p, dev, sms, st);
-    case 41: return launch_moe_few<4, kHalves, kUp, kGated>(W, p, dev, sms, st);
-    default:
-      if constexpr (kHalves == 1) return launch_moe_few<8, 1, kUp, kGated>(W, p, dev, sms, st);
   }
-  return invalid("fp8q_moe_layer: no such tiles");   // not reached: a gated unit has two weight tiles and four n-tiles at most
+  if constexpr (kHalves == 1) {   // a gated unit has two weight tiles at least and four n-tiles at most
+    switch (t.nt) {
+      case 1: return launch_moe_few<1, 1, kUp, kGated>(W, p, dev, sms, st);
+      case 2: return launch_moe_few<2, 1, kUp, kGated>(W, p, dev, sms, st);
+      case 4: return launch_moe_few<4, 1, kUp, kGated>(W, p, dev, sms, st);
+      default: return launch_moe_few<8, 1, kUp, kGated>(W, p, dev, sms, st);
+    }
+  }
+  return invalid("fp8q_moe_layer: no such tiles");   // (not reached)
 }
 
 }  // namespace

@@ -60,6 +60,7 @@ constexpr int kMfThreads = kMfConsumers + kMfEpiThreads + 32;   // + the warp th
 constexpr int kMfMaxRows = 1024;       // T * topk
 constexpr int kMfMaxTopk = 8;
 constexpr int kMfMaxExperts = 1024;
+static_assert(kMfMaxRows <= 1024 && kMfMaxExperts <= 1024, "rows and experts are packed in 10 bits each (mf_seg, mf_schedule)");
 constexpr int kMfFuseTokens = 16;      // and units a CTA of the down projection, at most,
 constexpr int kMfFuseUnits = 3;        // for it to add the rows up
 constexpr int kMfStageBytes = 32768;   // RU weight rows x 32 KB / RU of K
