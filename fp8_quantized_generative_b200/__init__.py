@@ -470,8 +470,10 @@ def moe_layer(X: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, Wq_
     [T,N] out.  Wq_up uint8 [E,F,K], or [E,2F,K] with gated=True (rows 0..F-1
     are activated and multiply rows F..2F-1), Wq_down uint8 [E,N,F], with
     per-channel scales s_up, s_down from quantize_weight_per_channel; residual
-    fp16 [T,N] is added (it may be `out` itself).  Larger batches: moe_route and
-    the grouped linears."""
+    fp16 [T,N] is added (it may be `out` itself).  Larger batches, and batches with
+    more than about ten rows an expert, where they are faster: moe_route and
+    the grouped linears, with the activation applied to the up projection's
+    output (they have none)."""
     act = _act(activation)
     try:
         dev = X.get_device()

@@ -16,9 +16,9 @@
 // streaming the chosen experts' weights once from HBM: 23 bytes a cycle and SM, a 32 KB
 // stage in 1400 cycles.  16 weight rows are the M operand of an MMA and up to 8
 // rows an n-tile.  The codes of both operands become fp16 (exact) and go through
-// mma.sync m16n8k16 with fp32 accumulators: on sm_100a its E4M3 form is emulated and
-// took 1110 cycles for the products of a stage where this form takes 650 to 740, so
-// that the stage's HBM time hides it.  A tcgen05 tile
+// mma.sync m16n8k16 with fp32 accumulators: its E4M3 form, without the conversions, was
+// measured at 1110 cycles for the products of a stage where this form takes 650 to 740,
+// so that the stage's HBM time hides it.  A tcgen05 tile
 // would read FP8 itself, but wants 64 or 128 weight rows to a tile, too coarse to
 // spread one token's experts over 148 SMs, and its issue takes 26-42 ns per 32 bytes
 // of K whatever the row count: 1.7 us and more on the one chain of K = 2048 that
